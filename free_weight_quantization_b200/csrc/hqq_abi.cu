@@ -283,7 +283,7 @@ extern "C" const char *hqq_strerror(int code) {
     case HQQ_ERR_ALIGN: return "misaligned pointer";
     case HQQ_ERR_WORKSPACE: return "workspace missing or too small";
     case HQQ_ERR_CUDA: return "CUDA launch or runtime error";
-    case HQQ_ERR_UNSUPPORTED: return "outside this library's limits (group_size <= 256, iters <= 64)";
+    case HQQ_ERR_UNSUPPORTED: return "outside this library's limits (stated in hqq_b200.h)";
     default: return "unknown error";
     }
 }

@@ -1,0 +1,301 @@
+// hqq_kv_store.cu -- the key/value cache: the check of its description, quantising rows as they
+// are written (hqq_kv_append) and reading them back (hqq_kv_read).
+//
+// Each group of a row starts from its least and largest value as a weight's group does, and its
+// codes are rounded against the scale and zero point as they are stored:
+//     scale = fp16(max(fl(fl(hi - lo) / (2^b - 1)), fl(max(|lo|, |hi|) 2^-10), 2^-24))
+//     zero  = fp16(fl(-lo inv)),  inv = fl(1 / scale)
+//     code  = clip(rint(fl(fl(x inv) + zero)), 0, 2^b - 1)
+// with fl() binary32 round to nearest even, one rounding for each operation, so that any program
+// that follows the same steps gets the same bits.  The second bound keeps the zero point of a
+// group of nearly equal values within +-1024 steps, where fp16 holds it to half a step; the last
+// is the least fp16.  Inputs are clamped to the fp16 range (a NaN becomes its lower end), so the
+// stored metadata are finite whatever is written.
+#include <algorithm>
+#include <type_traits>
+
+#include "hqq_kv.cuh"
+
+namespace hqq_kv {
+
+int check_cache(const hqq_kv_cache_t *cache, Cache *c) {
+    if (!cache) return HQQ_ERR_ARG;
+    if (cache->num_pages < 0 || cache->kv_heads <= 0 || cache->page_size <= 0) return HQQ_ERR_ARG;
+    if (cache->nbits < 1 || cache->nbits > 8 || cache->group_size <= 0 || cache->head_dim <= 0 ||
+        cache->head_dim % cache->group_size)
+        return HQQ_ERR_ARG;
+    if (cache->nbits != 2 && cache->nbits != 4 && cache->nbits != 8) return HQQ_ERR_UNSUPPORTED;
+    if (cache->head_dim != 64 && cache->head_dim != 128 && cache->head_dim != 256) return HQQ_ERR_UNSUPPORTED;
+    if (cache->group_size != 32 && cache->group_size != 64 && cache->group_size != 128) return HQQ_ERR_UNSUPPORTED;
+    int shift = 0;
+    while ((1 << shift) < cache->page_size && shift < 12) ++shift;
+    if ((1 << shift) != cache->page_size || shift < 4 || shift > 10) return HQQ_ERR_UNSUPPORTED;
+    // rows are counted in 40 bits: byte offsets stay far inside 64
+    if (cache->kv_heads > 65535 || cache->num_pages > (int64_t(1) << 40) / cache->page_size / cache->kv_heads)
+        return HQQ_ERR_UNSUPPORTED;
+    const void *p[4] = {cache->k_codes, cache->v_codes, cache->k_meta, cache->v_meta};
+    for (const void *q : p) {
+        if (cache->num_pages > 0 && !q) return HQQ_ERR_ARG;
+        if (!aligned_to(q, 16)) return HQQ_ERR_ALIGN;
+    }
+    c->codes[0] = (uint8_t *)cache->k_codes;
+    c->codes[1] = (uint8_t *)cache->v_codes;
+    c->meta[0] = (__half2 *)cache->k_meta;
+    c->meta[1] = (__half2 *)cache->v_meta;
+    c->pages = cache->num_pages;
+    c->page_shift = shift;
+    c->heads = cache->kv_heads;
+    return HQQ_OK;
+}
+
+}  // namespace hqq_kv
+
+namespace {
+
+using namespace hqq_kv;
+
+constexpr int kStoreThreads = 256;
+constexpr int kPerThread = 8;  // values of a row that one thread holds: 16 bytes
+
+struct StoreArgs {
+    Cache c;
+    const uint16_t *x[2];       // append: keys and values, strided
+    int64_t token_stride[2], head_stride[2];
+    uint16_t *y[2];             // values as read back, [tokens][heads][D]; null: not wanted
+    const int64_t *slots;
+    int64_t tokens;
+    bool wide;                  // x can be read 16 bytes at a time
+};
+
+// bytes [0, N) of v to p, aligned to N
+template <int N>
+__device__ __forceinline__ void put(uint8_t *p, uint64_t v) {
+    if constexpr (N == 1) *p = (uint8_t)v;
+    else if constexpr (N == 2) *(uint16_t *)p = (uint16_t)v;
+    else if constexpr (N == 4) *(uint32_t *)p = (uint32_t)v;
+    else *(uint64_t *)p = v;
+}
+
+template <int N>
+__device__ __forceinline__ uint64_t take(const uint8_t *p) {
+    if constexpr (N == 1) return __ldg(p);
+    else if constexpr (N == 2) return __ldg((const uint16_t *)p);
+    else if constexpr (N == 4) return __ldg((const uint32_t *)p);
+    else return __ldg((const unsigned long long *)p);
+}
+
+// byte offset within a row's codes of element d
+template <int D, int NB, int NG, int P>
+__device__ __forceinline__ int code_byte(int d) {
+    constexpr int g = D / NG, s = g / P;
+    return ((d % g) / s * (D / P) + d / g * s + d % s) * NB / 8;
+}
+
+// The 8 codes of elements d .. d+7 (lowest in the lowest bits) to or from a row.  A run of g / P
+// elements is stored together: 8 codes lie in one place, or in two where a run has 4.
+template <int D, int NB, int NG, int P>
+__device__ __forceinline__ void put_codes(uint8_t *row, int d, uint64_t codes) {
+    if constexpr (D / NG / P >= 8) {
+        put<NB>(row + code_byte<D, NB, NG, P>(d), codes);
+    } else {
+        put<NB / 2>(row + code_byte<D, NB, NG, P>(d), codes);
+        put<NB / 2>(row + code_byte<D, NB, NG, P>(d + 4), codes >> (4 * NB));
+    }
+}
+
+template <int D, int NB, int NG, int P>
+__device__ __forceinline__ uint64_t take_codes(const uint8_t *row, int d) {
+    if constexpr (D / NG / P >= 8) {
+        return take<NB>(row + code_byte<D, NB, NG, P>(d));
+    } else {
+        return take<NB / 2>(row + code_byte<D, NB, NG, P>(d)) |
+               take<NB / 2>(row + code_byte<D, NB, NG, P>(d + 4)) << (4 * NB);
+    }
+}
+
+// (code - zero) * scale of 8 codes, rounded once more to 16 bits
+template <int NB, bool BF>
+__device__ __forceinline__ uint4 values_of(uint64_t codes, float scale, float zero) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t c = (uint32_t)(codes >> (NB * (2 * i + j))) & ((1u << NB) - 1u);
+            const float q = __uint_as_float(0x4B000000u | c) - 8388608.0f;  // c, exactly
+            h[j] = from_f32<BF>(__fmul_rn(__fsub_rn(q, zero), scale));
+        }
+        w[i] = h[0] | h[1] << 16;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Quantises 8 values of one row; the D/NG/8 threads of its group are neighbours in a warp.
+template <int D, int NB, int NG, int P, bool BF>
+__device__ __forceinline__ void append_part(const StoreArgs &a, int side, int64_t token, int head, int d,
+                                            int64_t row, bool inside, bool live, const uint4 raw) {
+    constexpr int g = D / NG;
+    constexpr float top = (float)((1 << NB) - 1);
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        x[i] = fminf(fmaxf(to_f32<BF>((uint16_t)(w[i / 2] >> (16 * (i & 1)))), -65504.0f), 65504.0f);
+    float lo = x[0], hi = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        lo = fminf(lo, x[i]);
+        hi = fmaxf(hi, x[i]);
+    }
+#pragma unroll
+    for (int m = 1; m < g / 8; m *= 2) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
+    }
+    const float step = __fdiv_rn(__fsub_rn(hi, lo), top);
+    const float least = __fmul_rn(fmaxf(fabsf(lo), fabsf(hi)), 0x1p-10f);
+    const __half scale_h = __float2half_rn(fmaxf(fmaxf(step, least), 0x1p-24f));
+    const float scale = __half2float(scale_h), inv = __frcp_rn(scale);
+    const __half zero_h = __float2half_rn(__fmul_rn(-lo, inv));
+    const float zero = __half2float(zero_h);
+    uint64_t codes = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float t = fminf(fmaxf(__fadd_rn(__fmul_rn(x[i], inv), zero), 0.0f), top);
+        const uint32_t c = __float_as_uint(t + 8388608.0f) & 0xFFu;  // rint, ties to even
+        codes |= (uint64_t)c << (NB * i);
+    }
+    if (live) {
+        put_codes<D, NB, NG, P>(a.c.codes[side] + row * (D * NB / 8), d, codes);
+        if (d % g == 0) a.c.meta[side][row * NG + d / g] = __halves2half2(scale_h, zero_h);
+    }
+    if (inside && a.y[side]) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (live) v = values_of<NB, BF>(codes, scale, zero);
+        *(uint4 *)(a.y[side] + (token * a.c.heads + head) * D + d) = v;
+    }
+}
+
+template <bool BF>
+__device__ __forceinline__ uint4 load8(const uint16_t *p, bool wide) {
+    if (wide) return __ldg((const uint4 *)p);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = (uint32_t)__ldg(p + 2 * i) | (uint32_t)__ldg(p + 2 * i + 1) << 16;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One thread for 8 values of a key and the same 8 of its value: D / 8 threads a row.  Bound by the
+// bytes it moves: every load and store of a warp covers whole 32-byte sectors, and two 16-byte
+// loads are in flight for each thread.
+template <int D, int NB, int NG, bool BF>
+__global__ void __launch_bounds__(kStoreThreads) hqq_kv_append_kernel(const StoreArgs a) {
+    constexpr int kRows = kStoreThreads / (D / kPerThread);
+    const int64_t rows = a.tokens * a.c.heads;
+    const int64_t r0 = (int64_t)blockIdx.x * kRows + threadIdx.x / (D / kPerThread);
+    const int64_t r = r0 < rows ? r0 : rows - 1;  // whole warps take part in the exchanges below
+    const int d = (int)(threadIdx.x % (D / kPerThread)) * kPerThread;
+    const int64_t token = r / a.c.heads;
+    const int head = (int)(r - token * a.c.heads);
+    const uint4 k = load8<BF>(a.x[0] + token * a.token_stride[0] + head * a.head_stride[0] + d, a.wide);
+    const uint4 v = load8<BF>(a.x[1] + token * a.token_stride[1] + head * a.head_stride[1] + d, a.wide);
+    const int64_t slot = __ldg(a.slots + token);
+    const int64_t page = slot >> a.c.page_shift;
+    const bool inside = r0 < rows, live = inside && slot >= 0 && page < a.c.pages;
+    const int64_t row = live ? row_of(a.c, page, head, (int)(slot & ((1 << a.c.page_shift) - 1))) : 0;
+    append_part<D, NB, NG, kKeyPieces, BF>(a, 0, token, head, d, row, inside, live, k);
+    append_part<D, NB, NG, kValuePieces, BF>(a, 1, token, head, d, row, inside, live, v);
+}
+
+template <int D, int NB, int NG, bool BF>
+__global__ void __launch_bounds__(kStoreThreads) hqq_kv_read_kernel(const StoreArgs a) {
+    constexpr int kRows = kStoreThreads / (D / kPerThread), g = D / NG;
+    const int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / (D / kPerThread);
+    if (r >= a.tokens * a.c.heads) return;
+    const int d = (int)(threadIdx.x % (D / kPerThread)) * kPerThread;
+    const int64_t token = r / a.c.heads;
+    const int head = (int)(r - token * a.c.heads);
+    const int64_t slot = __ldg(a.slots + token);
+    const int64_t page = slot >> a.c.page_shift;
+    uint4 k = make_uint4(0, 0, 0, 0), v = k;
+    if (slot >= 0 && page < a.c.pages) {
+        const int64_t row = row_of(a.c, page, head, (int)(slot & ((1 << a.c.page_shift) - 1)));
+        const uint64_t kc = take_codes<D, NB, NG, kKeyPieces>(a.c.codes[0] + row * (D * NB / 8), d);
+        const uint64_t vc = take_codes<D, NB, NG, kValuePieces>(a.c.codes[1] + row * (D * NB / 8), d);
+        const float2 km = __half22float2(__ldg(a.c.meta[0] + row * NG + d / g));
+        const float2 vm = __half22float2(__ldg(a.c.meta[1] + row * NG + d / g));
+        k = values_of<NB, BF>(kc, km.x, km.y);
+        v = values_of<NB, BF>(vc, vm.x, vm.y);
+    }
+    if (a.y[0]) *(uint4 *)(a.y[0] + r * D + d) = k;
+    if (a.y[1]) *(uint4 *)(a.y[1] + r * D + d) = v;
+}
+
+template <bool APPEND>
+int launch_store(const hqq_kv_cache_t &cache, const StoreArgs &a, bool bf, cudaStream_t st) {
+    return with_layout(cache, [&](auto dim, auto bits, auto groups) {
+        constexpr int D = dim, NB = bits, NG = groups, kRows = kStoreThreads / (D / kPerThread);
+        const unsigned blocks = (unsigned)((a.tokens * a.c.heads + kRows - 1) / kRows);
+        if constexpr (APPEND) {
+            if (bf) hqq_kv_append_kernel<D, NB, NG, true><<<blocks, kStoreThreads, 0, st>>>(a);
+            else hqq_kv_append_kernel<D, NB, NG, false><<<blocks, kStoreThreads, 0, st>>>(a);
+        } else {
+            if (bf) hqq_kv_read_kernel<D, NB, NG, true><<<blocks, kStoreThreads, 0, st>>>(a);
+            else hqq_kv_read_kernel<D, NB, NG, false><<<blocks, kStoreThreads, 0, st>>>(a);
+        }
+        return cudaGetLastError() == cudaSuccess ? HQQ_OK : HQQ_ERR_CUDA;
+    });
+}
+
+int check_tokens(const Cache &c, int64_t tokens, int dtype) {
+    if (tokens < 0 || (dtype != HQQ_FP16 && dtype != HQQ_BF16)) return HQQ_ERR_ARG;
+    if (tokens > INT32_MAX / c.heads) return HQQ_ERR_UNSUPPORTED;
+    return HQQ_OK;
+}
+
+}  // namespace
+
+extern "C" int hqq_kv_append(const hqq_kv_cache_t *cache, const void *k, const void *v, int dtype,
+                             int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
+                             int64_t v_token_stride, int64_t v_head_stride, const int64_t *slots,
+                             void *k_values, void *v_values, void *stream) {
+    StoreArgs a = {};
+    int rc = check_cache(cache, &a.c);
+    if (rc == HQQ_OK) rc = check_tokens(a.c, tokens, dtype);
+    if (rc != HQQ_OK) return rc;
+    if (tokens == 0) return HQQ_OK;
+    if (!k || !v || !slots) return HQQ_ERR_ARG;
+    if (!aligned_to(k, 2) || !aligned_to(v, 2) || !aligned_to(slots, 8) || !aligned_to(k_values, 16) ||
+        !aligned_to(v_values, 16))
+        return HQQ_ERR_ALIGN;
+    a.x[0] = (const uint16_t *)k;
+    a.x[1] = (const uint16_t *)v;
+    a.token_stride[0] = k_token_stride;
+    a.token_stride[1] = v_token_stride;
+    a.head_stride[0] = k_head_stride;
+    a.head_stride[1] = v_head_stride;
+    a.y[0] = (uint16_t *)k_values;
+    a.y[1] = (uint16_t *)v_values;
+    a.slots = slots;
+    a.tokens = tokens;
+    a.wide = aligned_to(k, 16) && aligned_to(v, 16) &&
+             (k_token_stride | k_head_stride | v_token_stride | v_head_stride) % 8 == 0;
+    return launch_store<true>(*cache, a, dtype == HQQ_BF16, (cudaStream_t)stream);
+}
+
+extern "C" int hqq_kv_read(const hqq_kv_cache_t *cache, const int64_t *slots, int64_t tokens, int dtype,
+                           void *k_out, void *v_out, void *stream) {
+    StoreArgs a = {};
+    int rc = check_cache(cache, &a.c);
+    if (rc == HQQ_OK) rc = check_tokens(a.c, tokens, dtype);
+    if (rc != HQQ_OK) return rc;
+    if (tokens == 0) return HQQ_OK;
+    if (!slots || (!k_out && !v_out)) return HQQ_ERR_ARG;
+    if (!aligned_to(slots, 8) || !aligned_to(k_out, 16) || !aligned_to(v_out, 16)) return HQQ_ERR_ALIGN;
+    a.y[0] = (uint16_t *)k_out;
+    a.y[1] = (uint16_t *)v_out;
+    a.slots = slots;
+    a.tokens = tokens;
+    return launch_store<false>(*cache, a, dtype == HQQ_BF16, (cudaStream_t)stream);
+}

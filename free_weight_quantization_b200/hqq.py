@@ -27,6 +27,14 @@ class HqqOpt(ctypes.Structure):
                 ("eps_tiny", ctypes.c_float), ("scale_max", ctypes.c_float)]
 
 
+class HqqKvCache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_meta", ctypes.c_void_p), ("v_meta", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("nbits", ctypes.c_int32), ("group_size", ctypes.c_int32)]
+
+
 class HqqError(RuntimeError):
     pass
 
@@ -47,6 +55,13 @@ SIGNATURES = {
     "hqq_gemv": (_I32, [_P, _P, _P, _I64, _I64, _I32, _I64, _I32, _P, _P, _P]),
     "hqq_gemm": (_I32, [_P, _P, _P, _I64, _I64, _I32, _I64, _I32, _P, _I64, _P, _P]),
     "hqq_shrink_lp": (_I32, [_P, _I64, ctypes.c_double, ctypes.c_double, _P, _P]),
+    "hqq_kv_append": (_I32, [_P, _P, _P, _I32, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _P]),
+    "hqq_kv_read": (_I32, [_P, _P, _I64, _I32, _P, _P, _P]),
+    "hqq_kv_attention_workspace_bytes": (_SZ, [_P, _I64, _I64, _I64, _I64, _I64, _I64]),
+    "hqq_kv_attention": (_I32, [_P, _P, _I32, _I64, _I64, _I64, _I64, _I64, _I64, _P, _I64, _I64, _P,
+                                _I64, _I64, ctypes.c_float, _P, _P, _P, _SZ, _P]),
+    "hqq_kv_prefix_attention": (_I32, [_P, _P, _I32, _I64, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P,
+                                       _I64, _I64, _P, _I64, ctypes.c_float, _P, _P, _P, _SZ, _P]),
     "hqq_strerror": (ctypes.c_char_p, [_I32]),
 }
 
@@ -256,3 +271,243 @@ def err_trace_ints(t: torch.Tensor, n: int) -> list[int]:
     """Exact per-round error sums (units of 2^-32) from the (low, high) uint64 pairs."""
     v = t.cpu().view(torch.int64).tolist()
     return [(v[2 * i] & (2 ** 64 - 1)) + ((v[2 * i + 1] & (2 ** 64 - 1)) << 64) for i in range(n)]
+
+
+# ---- the key/value cache (hqq_kv_* in the header) ------------------------------------------
+
+_KV_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+
+
+class KVCache:
+    """A paged, group-quantized key/value cache: the tensors that the header's hqq_kv_cache
+    describes, and that description.
+
+    k_codes, v_codes: uint8 [pages, kv_heads, page_size, head_dim * nbits / 8]; k_meta, v_meta:
+    float16 [pages, kv_heads, page_size, head_dim / group_size, 2], (scale, zero).  Contiguous, on
+    one CUDA device; hqq_kv_cache() allocates them."""
+
+    __slots__ = ("k_codes", "v_codes", "k_meta", "v_meta", "num_pages", "kv_heads", "page_size",
+                 "head_dim", "nbits", "group_size", "device", "_c", "_ref")
+
+    def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_meta: torch.Tensor,
+                 v_meta: torch.Tensor, nbits: int, group_size: int):
+        if nbits not in (2, 4, 8):
+            raise HqqError("KVCache: nbits must be 2, 4 or 8")
+        if group_size not in (32, 64, 128):
+            raise HqqError("KVCache: group_size must be 32, 64 or 128")
+        if k_codes.dim() != 4:
+            raise HqqError("KVCache: codes must be [pages, kv_heads, page_size, head_dim * nbits / 8]")
+        pages, heads, page_size, row = k_codes.shape
+        head_dim = row * 8 // nbits
+        if head_dim not in (64, 128, 256) or row * 8 % nbits or head_dim % group_size:
+            raise HqqError("KVCache: head_dim must be 64, 128 or 256 and a multiple of group_size")
+        if heads < 1 or not 16 <= page_size <= 1024 or page_size & (page_size - 1):
+            raise HqqError("KVCache: page_size must be a power of two from 16 to 1024, kv_heads at least 1")
+        meta = (pages, heads, page_size, head_dim // group_size, 2)
+        for name, t, shape, dtype in (("k_codes", k_codes, k_codes.shape, torch.uint8),
+                                      ("v_codes", v_codes, k_codes.shape, torch.uint8),
+                                      ("k_meta", k_meta, meta, torch.float16),
+                                      ("v_meta", v_meta, meta, torch.float16)):
+            if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+                raise HqqError(f"KVCache: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+            if not t.is_cuda or t.device != k_codes.device:
+                raise HqqError("KVCache: the tensors must live on one CUDA device")
+        self.k_codes, self.v_codes, self.k_meta, self.v_meta = k_codes, v_codes, k_meta, v_meta
+        self.num_pages, self.kv_heads, self.page_size = pages, heads, page_size
+        self.head_dim, self.nbits, self.group_size = head_dim, nbits, group_size
+        self.device = k_codes.device
+        self._c = HqqKvCache(k_codes.data_ptr(), v_codes.data_ptr(), k_meta.data_ptr(), v_meta.data_ptr(),
+                             pages, page_size, heads, head_dim, nbits, group_size)
+        self._ref = ctypes.addressof(self._c)
+
+
+def hqq_kv_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, nbits: int = 4,
+                 group_size: int = 64, device="cuda") -> KVCache:
+    """An empty KVCache (every row reads as zeros)."""
+    if num_pages < 0 or nbits not in (2, 4, 8) or group_size not in (32, 64, 128) or head_dim % group_size:
+        raise HqqError("hqq_kv_cache: nbits must be 2, 4 or 8, group_size 32, 64 or 128 and divide head_dim")
+    codes = (num_pages, kv_heads, page_size, head_dim * nbits // 8)
+    meta = (num_pages, kv_heads, page_size, head_dim // group_size, 2)
+    return KVCache(torch.zeros(codes, dtype=torch.uint8, device=device),
+                   torch.zeros(codes, dtype=torch.uint8, device=device),
+                   torch.zeros(meta, dtype=torch.float16, device=device),
+                   torch.zeros(meta, dtype=torch.float16, device=device), nbits, group_size)
+
+
+def _kv_call(fn, device: torch.device, stream: torch.cuda.Stream | None, args, empties):
+    """Allocates the tensors of `empties` (shape, dtype) on the launching stream, so that their
+    memory is reused in its order, and runs fn(*args, pointers of those tensors, stream) with
+    `device` as the current device.  args(tensors) gives the arguments before the stream."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _kv_call(fn, device, stream, args, empties)
+    if stream is not None:
+        if stream.device != device:
+            raise HqqError(f"{fn.__name__}: the stream must belong to the cache's device")
+        with torch.cuda.stream(stream):
+            made = [None if e is None else torch.empty(e[0], dtype=e[1], device=device) for e in empties]
+        handle = stream.cuda_stream
+    else:
+        made = [None if e is None else torch.empty(e[0], dtype=e[1], device=device) for e in empties]
+        handle = torch.cuda.current_stream(device).cuda_stream
+    rc = fn(*args(made), handle)
+    if rc != HQQ_OK:
+        _check(rc, fn.__name__)
+    return made
+
+
+def _kv_rows(what: str, cache: KVCache, t: torch.Tensor, tokens: int):
+    if t.dtype not in _KV_DTYPES or t.device != cache.device:
+        raise HqqError(f"{what} must be a float16 or bfloat16 tensor on the cache's device")
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[1] != cache.kv_heads or t.shape[2] != cache.head_dim:
+        raise HqqError(f"{what} must be [tokens, kv_heads, head_dim]")
+    if t.stride(2) != 1 and t.numel():
+        raise HqqError(f"{what}: the values of a head must be contiguous")
+
+
+def _kv_out(what: str, t: torch.Tensor, shape, dtype, device):
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise HqqError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the cache's device")
+
+
+def _kv_slots(cache: KVCache, slots: torch.Tensor):
+    if slots.dtype != torch.int64 or slots.device != cache.device or slots.dim() != 1 or not slots.is_contiguous():
+        raise HqqError("slots must be a contiguous 1-D int64 tensor on the cache's device")
+    return slots.shape[0]
+
+
+def hqq_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, *,
+                  return_values: bool = False, out: tuple[torch.Tensor, torch.Tensor] | None = None,
+                  stream: torch.cuda.Stream | None = None):
+    """Quantizes keys and values [tokens, kv_heads, head_dim] (fp16 or bf16; tokens and heads may be
+    strided, as slices of a fused projection are) into `slots` (int64 page * page_size + offset;
+    negative: skipped) of the cache.  With return_values (or out=(k, v)) also returns the values that
+    the cache now stands for.  See hqq_kv_append in the header."""
+    tokens = _kv_slots(cache, slots)
+    _kv_rows("k", cache, k, tokens)
+    _kv_rows("v", cache, v, tokens)
+    if k.dtype != v.dtype:
+        raise HqqError("k and v must have the same type")
+    shape = (tokens, cache.kv_heads, cache.head_dim)
+    want = None
+    if out is not None:
+        for name, t in zip(("out[0]", "out[1]"), out, strict=True):
+            _kv_out(name, t, shape, k.dtype, cache.device)
+    elif return_values:
+        want = (shape, k.dtype)
+    ks, vs = k.stride(), v.stride()
+
+    def args(made):
+        kv = out if out is not None else made
+        return (cache._ref, k.data_ptr(), v.data_ptr(), _KV_DTYPES[k.dtype], tokens, ks[0], ks[1], vs[0], vs[1],
+                slots.data_ptr(), None if kv[0] is None else kv[0].data_ptr(),
+                None if kv[1] is None else kv[1].data_ptr())
+    made = _kv_call(lib().hqq_kv_append, cache.device, stream, args, (want, want))
+    return out if out is not None else tuple(made) if return_values else None
+
+
+def hqq_kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.float16, *,
+                out: tuple[torch.Tensor, torch.Tensor] | None = None,
+                stream: torch.cuda.Stream | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The keys and values [tokens, kv_heads, head_dim] that the cache's `slots` stand for (zeros for
+    a negative slot).  See hqq_kv_read in the header."""
+    tokens = _kv_slots(cache, slots)
+    if dtype not in _KV_DTYPES:
+        raise HqqError("dtype must be float16 or bfloat16")
+    shape, want = (tokens, cache.kv_heads, cache.head_dim), None
+    if out is not None:
+        for name, t in zip(("out[0]", "out[1]"), out, strict=True):
+            _kv_out(name, t, shape, dtype, cache.device)
+    else:
+        want = (shape, dtype)
+
+    def args(made):
+        kv = out if out is not None else made
+        return (cache._ref, slots.data_ptr(), tokens, _KV_DTYPES[dtype], kv[0].data_ptr(), kv[1].data_ptr())
+    made = _kv_call(lib().hqq_kv_read, cache.device, stream, args, (want, want))
+    return out if out is not None else tuple(made)
+
+
+def _kv_attend(cache: KVCache, q, pages, lens, prefix, window, scale, max_len, out, return_lse,
+               workspace, stream):
+    dev = cache.device
+    if q.dtype not in _KV_DTYPES or q.device != dev or q.dim() != 4 or q.shape[3] != cache.head_dim:
+        raise HqqError("q must be a float16 or bfloat16 tensor [batch, nq, heads, head_dim] on the cache's device")
+    batch, nq, heads, dim = q.shape
+    if heads < 1 or heads % cache.kv_heads:
+        raise HqqError("heads must be a positive multiple of the cache's kv_heads")
+    if q.stride(3) != 1 and q.numel():
+        raise HqqError("q: the values of a head must be contiguous")
+    if pages.dtype != torch.int32 or pages.device != dev or pages.dim() != 2 or pages.shape[0] != batch \
+            or (pages.shape[1] > 1 and pages.stride(1) != 1):
+        raise HqqError("pages must be an int32 tensor [batch, max_pages] on the cache's device, rows contiguous")
+    if lens.dtype != torch.int32 or lens.device != dev or lens.shape != (batch,) or not lens.is_contiguous():
+        raise HqqError("lens must be a contiguous int32 tensor [batch] on the cache's device")
+    room = pages.shape[1] * cache.page_size
+    if max_len is None:
+        max_len = room
+    elif not 0 <= max_len <= room:
+        raise HqqError("max_len must lie between 0 and max_pages * page_size")
+    if window < 0:
+        raise HqqError("window must not be negative (0: none)")
+    if scale is None:
+        scale = dim ** -0.5
+    prefix_len = 0
+    if prefix is not None:
+        prefix_pages, prefix_len = prefix
+        if prefix_pages.dtype != torch.int32 or prefix_pages.device != dev or prefix_pages.dim() != 1 \
+                or not prefix_pages.is_contiguous():
+            raise HqqError("prefix_pages must be a contiguous 1-D int32 tensor on the cache's device")
+        if not 0 <= prefix_len <= prefix_pages.shape[0] * cache.page_size:
+            raise HqqError("prefix_len must lie between 0 and the tokens of prefix_pages")
+    L = lib()
+    need = L.hqq_kv_attention_workspace_bytes(cache._ref, batch, nq, heads, max_len, window, prefix_len)
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise HqqError("workspace must be a contiguous tensor on the cache's device")
+    if out is not None:
+        _kv_out("out", out, q.shape, q.dtype, dev)
+    empties = (None if out is not None else (q.shape, q.dtype),
+               ((batch, nq, heads), torch.float32) if return_lse else None,
+               (need, torch.uint8) if workspace is None and need else None)
+    qs = q.stride()
+
+    def args(made):
+        o, lse, ws = made
+        o = out if out is not None else o
+        ws = workspace if workspace is not None else ws
+        head = (cache._ref, q.data_ptr(), _KV_DTYPES[q.dtype], batch, nq, heads, qs[0], qs[1], qs[2])
+        table = (pages.data_ptr(), pages.stride(0), pages.shape[1], lens.data_ptr(), max_len)
+        tail = (scale, o.data_ptr(), None if lse is None else lse.data_ptr(),
+                None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size())
+        if prefix is None:
+            return (*head, *table, window, *tail)
+        return (*head, prefix_pages.data_ptr(), prefix_len, *table, *tail)
+    fn = L.hqq_kv_attention if prefix is None else L.hqq_kv_prefix_attention
+    made = _kv_call(fn, dev, stream, args, empties)
+    o = out if out is not None else made[0]
+    return (o, made[1]) if return_lse else o
+
+
+def hqq_kv_attention(cache: KVCache, q: torch.Tensor, pages: torch.Tensor, lens: torch.Tensor, *,
+                     window: int = 0, scale: float | None = None, max_len: int | None = None,
+                     out: torch.Tensor | None = None, return_lse: bool = False,
+                     workspace: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
+    """Attention of the last nq tokens of each sequence, q [batch, nq, heads, head_dim] (fp16 or bf16,
+    strided in all but the last dimension), over its cached context: pages int32 [batch, max_pages],
+    lens int32 [batch] with the queries' own tokens counted.  Returns out (and, with return_lse, the
+    binary32 log-sum-exp [batch, nq, heads]).  scale defaults to head_dim ** -0.5; max_len bounds lens
+    (default: what `pages` has room for) and sizes the launch.  See hqq_kv_attention in the header."""
+    return _kv_attend(cache, q, pages, lens, None, window, scale, max_len, out, return_lse,
+                      workspace, stream)
+
+
+def hqq_kv_prefix_attention(cache: KVCache, q: torch.Tensor, prefix_pages: torch.Tensor, prefix_len: int,
+                            pages: torch.Tensor, lens: torch.Tensor, *, scale: float | None = None,
+                            max_len: int | None = None, out: torch.Tensor | None = None,
+                            return_lse: bool = False, workspace: torch.Tensor | None = None,
+                            stream: torch.cuda.Stream | None = None):
+    """hqq_kv_attention for a batch whose sequences share their first prefix_len tokens, held in
+    prefix_pages (int32 [n]) and read once for all; pages and lens are each sequence's own tokens
+    behind it.  See hqq_kv_prefix_attention in the header."""
+    return _kv_attend(cache, q, pages, lens, (prefix_pages, prefix_len), 0, scale, max_len,
+                      out, return_lse, workspace, stream)

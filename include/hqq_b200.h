@@ -218,6 +218,112 @@ int hqq_quantize_noalloc(const void *W, int64_t rows, int64_t cols, int nbits, i
  */
 int hqq_shrink_lp(const float *r, int64_t n, double beta, double p, float *out, void *stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * A key/value cache in the same representation: a decoder with quantized weights keeps the keys
+ * and values of its context as group-quantized codes with fp16 metadata (scale, zero), each row
+ * (one token's key or value of one head) standing for (code - zero) * scale.  It is paged: a pool
+ * of pages of page_size tokens, which sequences hold in any order.
+ *
+ *   codes [num_pages][kv_heads][page_size][head_dim * nbits / 8] bytes, for keys and for values
+ *   meta  [num_pages][kv_heads][page_size][head_dim / group_size][2] fp16 (scale, zero)
+ *   nbits 2, 4 or 8; head_dim 64, 128 or 256; group_size 32, 64 or 128, dividing head_dim;
+ *   page_size a power of two, 16 to 1024; every pointer 16-byte aligned.
+ * Element d = c * group_size + p * (group_size / P) + i of a row (0 <= i < group_size / P) is its
+ * code number p * (head_dim / P) + c * (group_size / P) + i, P = 4 for keys and 8 for values, and
+ * codes are packed lowest number in the lowest bits.  A slot is page * page_size + offset.
+ *
+ * The calls follow the conventions above.  Values are fp16 or bf16 (dtype HQQ_FP16, HQQ_BF16).
+ * Nothing read from the device (slots, page numbers, lengths) can make a kernel access memory
+ * outside the buffers described: what is out of range is left out, as stated at each call.
+ */
+#define HQQ_FP16 0
+#define HQQ_BF16 1
+
+typedef struct hqq_kv_cache {
+    void *k_codes, *v_codes, *k_meta, *v_meta; /* device pointers */
+    int64_t num_pages;
+    int32_t page_size, kv_heads, head_dim, nbits, group_size;
+} hqq_kv_cache_t;
+
+/*
+ * Quantizes the keys and values of `tokens` tokens into the cache's slots.  For each group, with
+ * each operation rounded to binary32 (fl) and inputs clamped to +-65504 (a NaN to -65504):
+ *     scale = fp16(max(fl(fl(max - min) / (2^nbits - 1)), fl(max(|max|, |min|) * 2^-10), 2^-24))
+ *     zero  = fp16(fl(-min * inv)),  inv = fl(1 / scale)
+ *     code  = clip(rint(fl(fl(x * inv) + zero)), 0, 2^nbits - 1)
+ *   k, v      [tokens][kv_heads][head_dim], 2-byte aligned, with the given strides (in values)
+ *             between tokens and heads; a head's values are contiguous
+ *   slots     [tokens] device int64; a token whose slot is negative or past the last page is not
+ *             written.  Slots are distinct: one that is named twice holds unspecified codes and
+ *             metadata afterwards
+ *   k_values, v_values  [tokens][kv_heads][head_dim] of dtype, 16-byte aligned, nullable
+ *             (outputs): what hqq_kv_read gives for these slots (zeros for a token not written)
+ * Returns HQQ_OK (tokens = 0: nothing launched) or an HQQ_ERR_* code.
+ */
+int hqq_kv_append(const hqq_kv_cache_t *cache, const void *k, const void *v, int dtype,
+                  int64_t tokens, int64_t k_token_stride, int64_t k_head_stride,
+                  int64_t v_token_stride, int64_t v_head_stride, const int64_t *slots,
+                  void *k_values, void *v_values, void *stream);
+
+/*
+ * Reads slots back: dtype(fl(fl(code - zero) * scale)), [tokens][kv_heads][head_dim]; zeros for a
+ * slot that is negative or past the last page.  k_out, v_out: 16-byte aligned, one may be null.
+ */
+int hqq_kv_read(const hqq_kv_cache_t *cache, const int64_t *slots, int64_t tokens, int dtype,
+                void *k_out, void *v_out, void *stream);
+
+/* Device workspace, in bytes, of the two calls below (0: none needed, or invalid arguments);
+ * window 0 for hqq_kv_prefix_attention, prefix_len 0 for hqq_kv_attention. */
+size_t hqq_kv_attention_workspace_bytes(const hqq_kv_cache_t *cache, int64_t batch, int64_t nq,
+                                        int64_t heads, int64_t max_len, int64_t window,
+                                        int64_t prefix_len);
+
+/*
+ * Attention of the last nq tokens of each sequence over its cached context:
+ *     out = sum_t p_t v_t / sum_t p_t,   p_t = exp(scale * q . k_t),   lse = log(sum_t p_t)
+ * k_t, v_t: the rows (code - zero) * scale, unrounded.  Query i of a sequence of len tokens is at
+ * position len - nq + i; it sees the tokens up to its own position, and with window > 0 only the
+ * last `window` of those.  Where it sees none, out is 0 and lse is -infinity.  The sums are
+ * binary32; on the value side p_t times the group's scale is rounded to fp16 (relative to the
+ * largest), once for codes and zero points alike.
+ *   q         [batch][nq][heads][head_dim], 2-byte aligned, with the given strides (in values);
+ *             heads a multiple of kv_heads, query head h reads key head h / (heads / kv_heads).
+ *             Finite values; a row with an infinity or a NaN has an unspecified result
+ *   pages     [batch][max_pages] device int32, rows pages_stride apart: each sequence's pages in
+ *             order.  Tokens of a page number outside the pool are not seen
+ *   lens      [batch] device int32: tokens of each sequence, the queries' own among them (append
+ *             them first).  Below 0 counts as 0, above max_len as max_len
+ *   max_len   at most max_pages * page_size: an upper bound on lens, which plans the launch
+ *   scale     > 0
+ *   out       [batch][nq][heads][head_dim] of dtype, 16-byte aligned (output)
+ *   lse       [batch][nq][heads] binary32, nullable (output)
+ *   workspace >= hqq_kv_attention_workspace_bytes(..) bytes, 16-byte aligned; contents on entry do
+ *             not matter; must not be used by anything else until this call's work has finished
+ * Results do not depend on what else runs: sums are joined in a fixed order.
+ * Limits: batch * kv_heads <= 65535, nq <= 65535, max_len < 2^31.
+ */
+int hqq_kv_attention(const hqq_kv_cache_t *cache, const void *q, int dtype, int64_t batch, int64_t nq,
+                     int64_t heads, int64_t q_batch_stride, int64_t q_token_stride,
+                     int64_t q_head_stride, const int32_t *pages, int64_t pages_stride,
+                     int64_t max_pages, const int32_t *lens, int64_t max_len, int64_t window,
+                     float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                     void *stream);
+
+/*
+ * The same for a batch whose sequences all begin with one prefix: sequence b is the prefix_len
+ * tokens of prefix_pages followed by its own lens[b] tokens of pages[b], and the prefix is read
+ * once for the whole batch.  prefix_pages: [ceil(prefix_len / page_size)] device int32; the last
+ * page may be partly filled (a sequence's own tokens begin on a page of their own).  The queries
+ * are the last nq tokens of prefix and own tokens together.
+ */
+int hqq_kv_prefix_attention(const hqq_kv_cache_t *cache, const void *q, int dtype, int64_t batch,
+                            int64_t nq, int64_t heads, int64_t q_batch_stride,
+                            int64_t q_token_stride, int64_t q_head_stride,
+                            const int32_t *prefix_pages, int64_t prefix_len, const int32_t *pages,
+                            int64_t pages_stride, int64_t max_pages, const int32_t *lens,
+                            int64_t max_len, float scale, void *out, float *lse, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
 /* Text for a return code (static storage). */
 const char *hqq_strerror(int code);
 
