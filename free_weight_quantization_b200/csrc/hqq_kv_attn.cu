@@ -23,10 +23,15 @@
 //   O^T = V^T W^T: lane 4r + j holds run r of the values of tokens 2j, 2j+1, 2j+8, 2j+9; pairs of
 //                 tokens are put side by side with one byte permute; W^T is S^T's layout, turned
 //                 by movmatrix.
-// The operands thus go from memory to registers and into the tensor cores: no shared memory, no
-// barriers in the loop.  Each warp takes every kWarps-th block of 16 tokens of its CTA's chunk and
-// keeps a running maximum and sum in binary32; they meet in shared memory at the end, and the
-// chunks of a long sequence in a second kernel, both in a fixed order.
+// Each warp brings its blocks of 16 tokens into a ring of its own in shared memory with 16-byte
+// asynchronous copies, several blocks ahead, and reads them from there as operands: no barriers
+// between warps in the loop.  It keeps a running maximum and sum in binary32; the warps of a CTA
+// meet in shared memory at the end.
+//
+// The tokens of all sequences and key heads are laid end to end in units of 64 and divided evenly
+// among as many CTAs as the GPU holds at once, whatever the lengths are; the lengths are read on
+// the device.  A pair of a sequence and a key head that is cut between CTAs leaves its parts in
+// the workspace, and hqq_kv_join_kernel joins them in the order of the tokens.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -39,8 +44,10 @@ namespace {
 using namespace hqq_kv;
 
 constexpr int kAttnWarps = 4, kAttnThreads = 32 * kAttnWarps;
-constexpr int kBlock = 16;          // tokens of one step of a warp
-constexpr float kNegInf = -INFINITY;
+constexpr int kBlock = 16;                      // tokens of one step of a warp
+constexpr int kUnit = kBlock * kAttnWarps;       // of one step of a CTA
+constexpr int kSms = 148;
+constexpr float kLowest = -1e30f;  // a maximum before any score
 // The running maximum may lag behind by this many powers of two before the sums are rescaled:
 // weights stay below 2^8 of what they are relative to.  w is kept within fp16 by 2^6 * 2^8 < 65504.
 constexpr float kLag = 8.0f;
@@ -51,29 +58,33 @@ struct Words {
     uint32_t w[N];
 };
 
-// the NBYTES of a lane's run, as 32-bit words (a run of 2 bytes: in the low half)
+// the 4 or fewer, 8 or 16 bytes of a piece of a lane's run, from shared memory (2 bytes: low half)
 template <int NBYTES>
-__device__ __forceinline__ Words<(NBYTES + 3) / 4> load_run(const uint8_t *p) {
-    Words<(NBYTES + 3) / 4> r;
-    if constexpr (NBYTES == 2) {
-        r.w[0] = __ldg((const uint16_t *)p);
-    } else if constexpr (NBYTES == 4) {
-        r.w[0] = __ldg((const uint32_t *)p);
-    } else if constexpr (NBYTES == 8) {
-        const uint2 v = __ldg((const uint2 *)p);
-        r.w[0] = v.x;
-        r.w[1] = v.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < NBYTES / 16; ++i) {
-            const uint4 v = __ldg((const uint4 *)p + i);
-            r.w[4 * i] = v.x;
-            r.w[4 * i + 1] = v.y;
-            r.w[4 * i + 2] = v.z;
-            r.w[4 * i + 3] = v.w;
-        }
-    }
-    return r;
+__device__ __forceinline__ void lds_piece(uint32_t *w, uint32_t at) {
+    if constexpr (NBYTES == 2) asm volatile("{.reg .u16 t; ld.shared.u16 t, [%1]; cvt.u32.u16 %0, t;}" : "=r"(w[0]) : "r"(at));
+    else if constexpr (NBYTES == 4) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at));
+    else if constexpr (NBYTES == 8) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+    else asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+}
+
+__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
+// A 32-bit word holds codes in two halves that an operand register takes side by side.  Code u of
+// byte h of the halves is brought to bit up(u): as high as it can be below the fp16 exponent at
+// one shift for two codes, because the tensor cores align a subnormal number as if its leading
+// bit were at the top, and what they drop is relative to that.  (Measured on scores, relative
+// error of the log-sum-exp at 2 / 4 bits: 5e-6 / 1e-6 with the codes where they lie.)
+template <int NB>
+__host__ __device__ constexpr int code_up(int u) {
+    return NB == 2 ? 6 + 2 * (u & 1) : NB == 4 ? 2 + 4 * (u & 1) : 0;
+}
+
+template <int NB>
+__device__ __forceinline__ uint32_t code_pair(uint32_t v, int h, int u) {
+    const int up = code_up<NB>(u), shift = up - (8 * h + NB * u);
+    return (shift >= 0 ? v << shift : v >> -shift) & ((((1u << NB) - 1u) * 0x00010001u) << up);
 }
 
 // How the D / 4 codes of a lane's run of a key become D / 8 operand registers of two codes each:
@@ -82,45 +93,58 @@ template <int D, int NB, int NG>
 struct KeyRegs {
     // a word whose halves belong to different groups is spread out first (2-bit codes, g = 32)
     static constexpr bool kSpread = D / NG / kKeyPieces < 32 / NB;
-    static constexpr int kSpan = kSpread ? 8 / NB : 16 / NB;  // registers of one 16- or 32-bit unit
     static constexpr int kU = 8 / NB;
-    __host__ __device__ static constexpr int lo(int x) {
-        return kSpread ? x / kSpan * 2 * kSpan + x % kSpan : x / kSpan * 2 * kSpan + x % kSpan;
-    }
+    static constexpr int kSpan = kSpread ? kU : 2 * kU;  // registers of one 16- or 32-bit unit
+    __host__ __device__ static constexpr int lo(int x) { return x / kSpan * 2 * kSpan + x % kSpan; }
     __host__ __device__ static constexpr int hi(int x) { return lo(x) + kSpan; }
-    __host__ __device__ static constexpr int up(int x) { return NB * (x % kU); }
+    __host__ __device__ static constexpr int up(int x) { return code_up<NB>(x % kU); }
     template <int N>
     __device__ static __forceinline__ uint32_t reg(const Words<N> &run, int x) {
-        constexpr uint32_t mask = ((1u << NB) - 1u) * 0x00010001u;
         if constexpr (kSpread) {
             const int unit = x / kSpan;
-            const uint32_t v = __byte_perm(run.w[unit / 2], 0, unit & 1 ? 0x4342 : 0x4140);
-            return v & (mask << up(x));
+            return code_pair<NB>(__byte_perm(run.w[unit / 2], 0, unit & 1 ? 0x4342 : 0x4140), 0, x % kU);
         } else {
-            const int y = x % kSpan;
-            return (run.w[x / kSpan] >> (y / kU * 8)) & (mask << up(x));
+            return code_pair<NB>(run.w[x / kSpan], x % kSpan / kU, x % kU);
         }
     }
 };
 
 // Code x of a lane's run of the values (D / 8 codes) of two tokens, side by side, scaled by
-// 2^(up(x) - 24).
+// 2^(up(x) - 24).  The run of the first token is `a` or `b`: sel_lo and sel_hi say which (the byte
+// permutes for the words' low and high halves).
 template <int NB>
 struct ValueRegs {
-    static constexpr int kU = 8 / NB, kSpan = 16 / NB;
-    __host__ __device__ static constexpr int up(int x) { return NB * (x % kU); }
+    static constexpr int kU = 8 / NB, kSpan = 2 * kU;
+    __host__ __device__ static constexpr int up(int x) { return code_up<NB>(x % kU); }
     template <int N>
-    __device__ static __forceinline__ uint32_t reg(const Words<N> &a, const Words<N> &b, int x) {
-        constexpr uint32_t mask = ((1u << NB) - 1u) * 0x00010001u;
-        const int unit = x / kSpan, y = x % kSpan;
-        const uint32_t v = __byte_perm(a.w[unit / 2], b.w[unit / 2], unit & 1 ? 0x7632 : 0x5410);
-        return (v >> (y / kU * 8)) & (mask << up(x));
+    __device__ static __forceinline__ uint32_t reg(const Words<N> &a, const Words<N> &b, int x, uint32_t sel_lo,
+                                                   uint32_t sel_hi) {
+        const int unit = x / kSpan;
+        return code_pair<NB>(__byte_perm(a.w[unit / 2], b.w[unit / 2], unit & 1 ? sel_hi : sel_lo), x % kSpan / kU, x % kU);
     }
 };
 
+// Where 16-byte chunk c of token t's row lies among the chunks of a block of 16 rows of n chunks,
+// so that a warp's reads of keys (lanes 4r + j: run j of token r) and of values (run r of token 2j
+// or 2j + 1, the odd lanes' two in the other order) meet in no bank.  The 8 chunks of a 128-byte
+// line are the banks of a 16-byte access.  Token t + 8 always lies 8 rows behind t.
+__host__ __device__ constexpr int key_chunk(int n, int t, int c) {
+    const int f = n == 8 ? (t & 1) : n == 16 ? (c >> 3) ^ 2 * (t & 1) : 0;
+    return t * n + (c ^ f);
+}
+
+__host__ __device__ constexpr int value_chunk(int n, int t, int c) {
+    const int p = (t >> 1) & 3;
+    if (n == 16) return t * n + (c ^ ((p & 1) | (p & 2) << 1));
+    if (n == 8) return t * n + (c ^ 2 * p);
+    if (n == 4) return t * n + (c ^ 2 * ((t >> 2) & 1));
+    if (n == 2) return (t * n + c) ^ 4 * ((t >> 2) & 1);
+    return t * n + c;
+}
+
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -129,7 +153,7 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 // the transpose of an 8 x 8 matrix of 16-bit values that the warp holds a row to four lanes
 __device__ __forceinline__ uint32_t turn(uint32_t v) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
 
@@ -161,28 +185,63 @@ __device__ __forceinline__ void visible(const Attn &a, int64_t len, int i, int64
     if (hi < 0) hi = 0;
 }
 
+// What a kernel of this layout keeps in shared memory and how many of its CTAs an SM holds.
 template <int D, int NB, int NG, int RB>
-struct Smem {
-    float o[kAttnWarps][8 * RB][D];
-    float m[kAttnWarps][8 * RB], l[kAttnWarps][8 * RB];
+struct Shape {
+    static constexpr int kRowBytes = D * NB / 8, kChunks = kRowBytes / 16;
+    static constexpr int kCodeBytes = kBlock * kRowBytes, kMetaBytes = kBlock * NG * 4;
+    static constexpr int kStage = 2 * (kCodeBytes + kMetaBytes);  // keys, values, their metadata
+    // blocks in flight: some 8 KB for each warp
+    static constexpr int kStages = kStage >= 6144 ? 2 : kStage >= 3072 ? 3 : kStage >= 1536 ? 4 : 6;
+    static constexpr int kRow = D + 4;  // floats of a row of results: 16-byte stores, two to a bank
+    static constexpr int kRing = kAttnWarps * kStages * kStage;
+    static constexpr int kResult = kAttnWarps * 8 * RB * (kRow + 2) * 4;
+    static constexpr int kSmem = kRing > kResult ? kRing : kResult;
+    static constexpr int kCtas = D == 256 || RB == 2 ? 2 : 4;
 };
 
+// units of one pair of sequence b: at least one, so that each pair has a CTA that writes its rows
+__device__ __forceinline__ int64_t units_of(const Attn &a, int b) {
+    int64_t span = own_len(a, b);
+    if (a.window > 0) span = min(span, a.window + a.nq + kBlock);
+    return max((span + kUnit - 1) / kUnit, (int64_t)1);
+}
+
+// the sum over sequences [0, n) of their pairs' units, for every thread of the CTA
+template <int THREADS>
+__device__ int64_t units_before(const Attn &a, int n, int64_t *shared) {
+    int64_t sum = 0;
+    for (int b = threadIdx.x; b < n; b += THREADS) sum += units_of(a, b);
+#pragma unroll
+    for (int x = 16; x > 0; x /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    sum = 0;
+    for (int w = 0; w < THREADS / 32; ++w) sum += shared[w];
+    return sum * a.row_blocks * a.c.heads;
+}
+
+// the last CTA whose share begins at unit x or before: CTA c has [total c / ctas, total (c + 1) / ctas)
+__device__ __forceinline__ int cta_of(int64_t x, int64_t total, int ctas) {
+    return (int)(((x + 1) * ctas - 1) / total);
+}
+
+// One segment: the blocks of tokens [first unit, last unit) of a pair, by all warps of the CTA.
+// `to_part`: where a result goes that is not the pair's whole; see the end.
 template <int D, int NB, int NG, int RB, bool PREFIX>
-__global__ void __launch_bounds__(kAttnThreads) hqq_kv_attn_kernel(const Attn a) {
-    constexpr int g = D / NG, KR = D / 8, VR = D / 8, RU = 8 * RB;
-    constexpr int kKeyBytes = D * NB / 32, kValueBytes = D * NB / 64, kRowBytes = D * NB / 8;
+__device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, int head, int64_t unit0, int64_t unit1,
+                                               float *part_o, float *part_lse, bool by_slot, unsigned char *smem) {
+    using S = Shape<D, NB, NG, RB>;
     using KRegs = KeyRegs<D, NB, NG>;
     using VRegs = ValueRegs<NB>;
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    auto &sm = *reinterpret_cast<Smem<D, NB, NG, RB> *>(smem_raw);
+    constexpr int g = D / NG, KR = D / 8, VR = D / 8, RU = 8 * RB, n = S::kChunks;
+    constexpr int kKeyBytes = S::kRowBytes / 4, kValueBytes = S::kRowBytes / 8;
+    constexpr int kKeyPiece = kKeyBytes < 16 ? kKeyBytes : 16, kValuePiece = kValueBytes < 16 ? kValueBytes : 16;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, j = lane & 3;
-    const int split = blockIdx.x, b0 = PREFIX ? 0 : (int)blockIdx.z / a.c.heads, head = (int)blockIdx.z % a.c.heads;
     const int unit_rows = a.nq * a.share;                       // rows of one sequence and key head
     const int total_rows = PREFIX ? a.batch * unit_rows : unit_rows;
-    const int row0 = (int)blockIdx.y * RU;
-    const int part = PREFIX ? split : a.prefix_splits + split;  // where the partial result goes
-    const int64_t all_rows = (int64_t)a.batch * a.nq * a.heads;
 
     // output row of local row l
     auto out_row = [&](int l) -> int64_t {
@@ -190,7 +249,7 @@ __global__ void __launch_bounds__(kAttnThreads) hqq_kv_attn_kernel(const Attn a)
         return ((int64_t)b * a.nq + i) * a.heads + head * a.share + h;
     };
 
-    // ---- the tokens of this chunk that some row of the block may see
+    // ---- the tokens of this segment that some row of the block may see
     const int last_row = min(row0 + RU, total_rows) - 1;
     int64_t first = 0, last;
     if constexpr (PREFIX) {
@@ -202,27 +261,60 @@ __global__ void __launch_bounds__(kAttnThreads) hqq_kv_attn_kernel(const Attn a)
         visible<PREFIX>(a, len, last_row / a.share, lo, last);
         last = min(last, len);
     }
-    const int64_t from = (first & ~(int64_t)(kBlock - 1)) + (int64_t)split * a.chunk;
-    const int64_t to = min(from + a.chunk, last);
-    if (from >= to) {  // nothing here: the chunk's weight is zero
-        if (a.part_lse) {
-            for (int l = row0 + (int)threadIdx.x; l <= last_row; l += kAttnThreads)
-                a.part_lse[part * all_rows + out_row(l)] = kNegInf;
-        } else {
-            for (int l = row0; l <= last_row; ++l) {
-                const int64_t o = out_row(l);
-                for (int d = threadIdx.x; d < D; d += kAttnThreads) a.out[o * D + d] = 0;
-                if (a.lse && threadIdx.x == 0) a.lse[o] = kNegInf;
+    const int64_t from = (first & ~(int64_t)(kBlock - 1)) + unit0 * kUnit;
+    const int64_t to = max(min(from + (unit1 - unit0) * kUnit, last), from);
+
+    // ---- copies: this warp's block number `it` of the segment into stage it % kStages
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (S::kStages * S::kStage);
+    const int steps = (int)((to - from + kBlock - 1) / kBlock - warp + kAttnWarps - 1) / kAttnWarps;
+    const int32_t *table = PREFIX ? a.prefix_pages : a.pages + b0 * a.pages_stride;
+    const int page_mask = (1 << a.c.page_shift) - 1;
+    int page_of_lane = 0;     // the page of block number it - it % 32 + lane
+    uint32_t there = 0;       // bit i: the page of the block copied i steps ago is in the pool
+    auto copy = [&](int it, int stage) {
+        there <<= 1;
+        if (it < steps) {
+            const int64_t t = from + (int64_t)(warp + it * kAttnWarps) * kBlock;
+            if ((it & 31) == 0) {
+                const int64_t tl = t + (int64_t)lane * kUnit;
+                page_of_lane = tl < to ? __ldg(table + (tl >> a.c.page_shift)) : -1;
+            }
+            const int page = __shfl_sync(0xffffffffu, page_of_lane, it & 31);
+            if (page >= 0 && page < a.c.pages) {
+                there |= 1u;
+                const int64_t row = row_of(a.c, page, head, (int)t & page_mask);
+                const uint32_t s = ring + stage * S::kStage;
+                const uint8_t *k = a.c.codes[0] + row * S::kRowBytes, *v = a.c.codes[1] + row * S::kRowBytes;
+#pragma unroll
+                for (int i = 0; i < (kBlock * n + 31) / 32; ++i) {
+                    const int at = lane + 32 * i;
+                    if (kBlock * n >= 32 || at < kBlock * n) {
+                        copy16(s + 16 * key_chunk(n, at / n, at % n), k + 16 * at);
+                        copy16(s + S::kCodeBytes + 16 * value_chunk(n, at / n, at % n), v + 16 * at);
+                    }
+                }
+                constexpr int mc = S::kMetaBytes / 16;  // chunks of metadata of each side
+#pragma unroll
+                for (int i = 0; i < (2 * mc + 31) / 32; ++i) {
+                    const int at = lane + 32 * i;
+                    if (2 * mc % 32 == 0 || at < 2 * mc) {
+                        const int side = at >= mc ? 1 : 0;
+                        copy16(s + 2 * S::kCodeBytes + 16 * at, (const uint8_t *)(a.c.meta[side] + row * NG) + 16 * (at - side * mc));
+                    }
+                }
             }
         }
-        return;
-    }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i) copy(i, i);
 
     // ---- the rows of this lane: as operand column r, and as result columns 2j and 2j + 1
-    uint32_t qb[RB][KR];      // q, paired as the keys' registers are
-    float qs[RB][2][NG];      // sum of q over each group, for result columns
-    float unit[RB][2];        // what a result is to be multiplied by: powers of two out
+    uint32_t qb[RB][KR];         // q, paired as the keys' registers are
+    float qs[RB][2][NG];         // sum of q over each group, for result columns
+    float unit[RB][2];           // what a result is to be multiplied by: powers of two out
     int hi_[RB][2], lo_[RB][2];  // visible tokens, relative to `from`
+    int all_lo = 0, all_hi = (int)(to - from);  // tokens that every row of the block sees
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
         const int l = row0 + 8 * rb + r;
@@ -231,21 +323,19 @@ __global__ void __launch_bounds__(kAttnThreads) hqq_kv_attn_kernel(const Attn a)
         const int b = b0 + lc / unit_rows, i = lc % unit_rows / a.share, h = head * a.share + lc % a.share;
         const uint16_t *q = a.q + b * a.q_batch + i * a.q_token + h * a.q_head;
         // each row is scaled by a power of two that takes its largest magnitude to [2^14, 2^15):
-        // exact, but for values 2^-22 below the largest, and it makes bf16 fit fp16
+        // exact, but for values 2^-20 below the largest, and it makes bf16 fit fp16
         float big = 0.0f;
 #pragma unroll
         for (int x = 0; x < KR; ++x) {
             const int e[2] = {KRegs::lo(x), KRegs::hi(x)};
-            float v[2];
+            uint32_t v[2];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 const int d = e[y] / (g / 4) * g + j * (g / 4) + e[y] % (g / 4);
-                const uint16_t raw = live ? __ldg(q + d) : (uint16_t)0;
-                v[y] = a.bf ? to_f32<true>(raw) : to_f32<false>(raw);
-                big = fmaxf(big, fabsf(v[y]));
+                v[y] = live ? (uint32_t)__ldg(q + d) : 0u;
+                big = fmaxf(big, fabsf(a.bf ? to_f32<true>((uint16_t)v[y]) : to_f32<false>((uint16_t)v[y])));
             }
-            qb[rb][x] = a.bf ? (__float_as_uint(v[0]) >> 16) | (__float_as_uint(v[1]) & 0xffff0000u)
-                             : (uint32_t)from_f32<false>(v[0]) | (uint32_t)from_f32<false>(v[1]) << 16;
+            qb[rb][x] = v[0] | v[1] << 16;
         }
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
@@ -276,9 +366,12 @@ __global__ void __launch_bounds__(kAttnThreads) hqq_kv_attn_kernel(const Attn a)
         const float un = 0x1p24f / up * a.scale_log2;
         int64_t lo, hi;
         visible<PREFIX>(a, own_len(a, b), i, lo, hi);
-        const int64_t cap = to - from;
-        const int rel_hi = live ? (int)min(max(hi - from, (int64_t)0), cap) : 0;
-        const int rel_lo = (int)min(max(lo - from, (int64_t)0), cap);
+        // a row that is not there (q = 0) may see everything: its result is not written
+        const int cap = (int)(to - from);
+        const int rel_hi = live ? (int)min(max(hi - from, (int64_t)0), (int64_t)cap) : cap;
+        const int rel_lo = live ? (int)min(max(lo - from, (int64_t)0), (int64_t)cap) : 0;
+        all_hi = min(all_hi, __reduce_min_sync(0xffffffffu, rel_hi));
+        all_lo = max(all_lo, __reduce_max_sync(0xffffffffu, rel_lo));
 #pragma unroll
         for (int y = 0; y < 2; ++y) {  // lane 4 (2j + y) holds row 2j + y
             const int src = 4 * (2 * j + y);
@@ -290,99 +383,129 @@ __global__ void __launch_bounds__(kAttnThreads) hqq_kv_attn_kernel(const Attn a)
         }
     }
 
-    float o[RB][VR / 2][4];   // O^T: rows are elements 2mb, 2mb + 1 of run r, columns rows 2j, 2j + 1
-    float oz[RB][2][NG];      // sum of w vz
-    float m[RB][2], l[RB][2];
+    // O^T: row r of an MMA's 16 is element 2mb of run r, row r + 8 element 2mb + 1; columns are rows
+    // 2j, 2j + 1.  oz: the same for the zero points, sum of w vz (each row of the 16 alike)
+    float o[RB][VR / 2][4], oz[RB][NG][4];
+    float m[RB][2], l[RB][2], bound[RB][2];  // bound: a raw score above it asks for a new maximum
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
 #pragma unroll
-        for (int x = 0; x < VR / 2; ++x)
+        for (int y = 0; y < 4; ++y) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) o[rb][x][y] = 0.0f;
+            for (int x = 0; x < VR / 2; ++x) o[rb][x][y] = 0.0f;
+#pragma unroll
+            for (int x = 0; x < NG; ++x) oz[rb][x][y] = 0.0f;
+        }
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-            m[rb][y] = kNegInf;
+            m[rb][y] = kLowest;
+            bound[rb][y] = -INFINITY;
             l[rb][y] = 0.0f;
-#pragma unroll
-            for (int x = 0; x < NG; ++x) oz[rb][y][x] = 0.0f;
         }
     }
     float vref = 0x1p-24f;    // a power of two, at least every value scale so far
+    float vin = kWeightUnit * 0x1p24f;
 
-    const int span = (int)(to - from);
-    const int blocks = (span + kBlock - 1) / kBlock;
-    const int32_t *table = PREFIX ? a.prefix_pages : a.pages + b0 * a.pages_stride;
-    int page_of_lane = 0;     // the page of this warp's block number it + lane - it % 32
-    for (int it = 0, blk = warp; blk < blocks; ++it, blk += kAttnWarps) {
-        if ((it & 31) == 0) {
-            const int64_t t = from + (int64_t)(blk + lane * kAttnWarps) * kBlock;
-            page_of_lane = t < to ? __ldg(table + (t >> a.c.page_shift)) : -1;
-        }
-        const int page = __shfl_sync(0xffffffffu, page_of_lane, it & 31);
-        if (page < 0 || page >= a.c.pages) continue;  // a page that is not there is not seen
-        const int t0 = blk * kBlock;                   // relative to `from`
-        const int64_t row = row_of(a.c, page, head, (int)((from + t0) & ((1 << a.c.page_shift) - 1)));
+    const uint32_t k_at = (uint32_t)(16 * key_chunk(n, r, j * kKeyBytes / 16) + j * kKeyBytes % 16);
+    // the odd lanes read the second token of a pair first
+    const int va = 2 * j + (j & 1), vb = 2 * j + 1 - (j & 1);
+    const uint32_t v_at[2] = {(uint32_t)(S::kCodeBytes + 16 * value_chunk(n, va, r * kValueBytes / 16) + r * kValueBytes % 16),
+                              (uint32_t)(S::kCodeBytes + 16 * value_chunk(n, vb, r * kValueBytes / 16) + r * kValueBytes % 16)};
+    const uint32_t sel_lo = j & 1 ? 0x1054u : 0x5410u, sel_hi = j & 1 ? 0x3276u : 0x7632u;
+    const uint32_t m_at = (uint32_t)(2 * S::kCodeBytes + r * NG * 4);
 
-        // ---- loads.  Rows of the page behind the last token hold anything: their codes are
-        // finite numbers, and their metadata are replaced by zeros
+    // one block: MASKED where some row does not see all of its tokens
+    auto step = [&](uint32_t s_at, int t0, auto masked) {
+        constexpr bool MASKED = decltype(masked)::value;
         Words<(kKeyBytes + 3) / 4> k0, k1;
-        Words<(kValueBytes + 3) / 4> v0, v1, v2, v3;
-        k0 = load_run<kKeyBytes>(a.c.codes[0] + (row + r) * kRowBytes + j * kKeyBytes);
-        k1 = load_run<kKeyBytes>(a.c.codes[0] + (row + r + 8) * kRowBytes + j * kKeyBytes);
-        v0 = load_run<kValueBytes>(a.c.codes[1] + (row + 2 * j) * kRowBytes + r * kValueBytes);
-        v1 = load_run<kValueBytes>(a.c.codes[1] + (row + 2 * j + 1) * kRowBytes + r * kValueBytes);
-        v2 = load_run<kValueBytes>(a.c.codes[1] + (row + 2 * j + 8) * kRowBytes + r * kValueBytes);
-        v3 = load_run<kValueBytes>(a.c.codes[1] + (row + 2 * j + 9) * kRowBytes + r * kValueBytes);
-        float2 km[2][NG], vm[2][NG];
+        Words<(kValueBytes + 3) / 4> v[4];
+#pragma unroll
+        for (int i = 0; i < kKeyBytes / kKeyPiece; ++i) {
+            // the chunks of a run lie together, or exchanged as the swizzle says
+            const uint32_t at = s_at + (kKeyBytes > 16 ? k_at ^ (uint32_t)(16 * i) : k_at);
+            lds_piece<kKeyPiece>(k0.w + 4 * i, at);
+            lds_piece<kKeyPiece>(k1.w + 4 * i, at + 8 * S::kRowBytes);
+        }
+#pragma unroll
+        for (int i = 0; i < (kValueBytes + kValuePiece - 1) / kValuePiece; ++i)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const uint32_t at = s_at + (kValueBytes > 16 ? v_at[y & 1] ^ (uint32_t)(16 * i) : v_at[y & 1]);
+                lds_piece<kValuePiece>(v[y].w + 4 * i, at + (y >> 1) * 8 * S::kRowBytes);
+            }
+        uint32_t km[2][NG], vm[2][NG];  // (scale, zero)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-            const int64_t t = from + t0 + r + 8 * y;
-            const bool there = t >= first && t < to;
+            constexpr int piece = NG >= 4 ? 16 : NG * 4;
 #pragma unroll
-            for (int x = 0; x < NG; ++x) {
-                km[y][x] = vm[y][x] = make_float2(0.0f, 0.0f);
-                if (there) {
-                    km[y][x] = __half22float2(__ldg(a.c.meta[0] + (row + r + 8 * y) * NG + x));
-                    vm[y][x] = __half22float2(__ldg(a.c.meta[1] + (row + r + 8 * y) * NG + x));
+            for (int x = 0; x < NG * 4 / piece; ++x) {
+                const uint32_t at = s_at + m_at + y * 8 * NG * 4 + x * 16;
+                lds_piece<piece>(km[y] + 4 * x, at);
+                lds_piece<piece>(vm[y] + 4 * x, at + S::kMetaBytes);
+            }
+            if constexpr (MASKED) {
+                // rows of a page that hold no token of this sequence hold anything: their codes are
+                // finite numbers, and their metadata are replaced by zeros
+                const int64_t t = from + t0 + r + 8 * y;
+                const bool live = t >= first && t < to;
+#pragma unroll
+                for (int x = 0; x < NG; ++x) {
+                    km[y][x] = live ? km[y][x] : 0u;
+                    vm[y][x] = live ? vm[y][x] : 0u;
                 }
             }
         }
+        auto meta = [](uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); };
 
-        // ---- S^T and its scores, in powers of two
+        // ---- S^T: raw scores
         float s[RB][4];
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
+        for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
             for (int y = 0; y < 4; ++y) s[rb][y] = 0.0f;
 #pragma unroll
-            for (int x = 0; x < NG; ++x) {
-                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int x = 0; x < NG; ++x) {
+            float c[RB][4];
 #pragma unroll
-                for (int st = x * (g / 16); st < (x + 1) * (g / 16); ++st)
-                    mma_16816(c, KRegs::reg(k0, 2 * st), KRegs::reg(k1, 2 * st), KRegs::reg(k0, 2 * st + 1),
-                              KRegs::reg(k1, 2 * st + 1), qb[rb][2 * st], qb[rb][2 * st + 1]);
+            for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    s[rb][y] = __fmaf_rn(km[y >> 1][x].x, __fmaf_rn(-km[y >> 1][x].y, qs[rb][y & 1][x], c[y]), s[rb][y]);
+                for (int y = 0; y < 4; ++y) c[rb][y] = 0.0f;
+#pragma unroll
+            for (int st = x * (g / 16); st < (x + 1) * (g / 16); ++st) {
+                const uint32_t a0 = KRegs::reg(k0, 2 * st), a1 = KRegs::reg(k1, 2 * st);
+                const uint32_t a2 = KRegs::reg(k0, 2 * st + 1), a3 = KRegs::reg(k1, 2 * st + 1);
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) mma_16816(c[rb], a0, a1, a2, a3, qb[rb][2 * st], qb[rb][2 * st + 1]);
             }
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-                const int t = t0 + r + 8 * (y >> 1);
-                const bool seen = t < hi_[rb][y & 1] && t >= lo_[rb][y & 1];
-                s[rb][y] = seen ? s[rb][y] * unit[rb][y & 1] : kNegInf;
+                const float2 z = meta(km[y >> 1][x]);
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb)
+                    s[rb][y] = __fmaf_rn(z.x, __fmaf_rn(-z.y, qs[rb][y & 1][x], c[rb][y]), s[rb][y]);
             }
         }
+        if constexpr (MASKED) {
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int t = t0 + r + 8 * (y >> 1);
+                    if (t >= hi_[rb][y & 1] || t < lo_[rb][y & 1]) s[rb][y] = -INFINITY;
+                }
+        }
         // ---- a new maximum, or a larger value scale than any before: rescale
-        float vs = 0.0f;
+        __half2 vs2 = __float2half2_rn(0.0f);
 #pragma unroll
         for (int y = 0; y < 2; ++y)
 #pragma unroll
-            for (int x = 0; x < NG; ++x) vs = fmaxf(vs, vm[y][x].x);
+            for (int x = 0; x < NG; ++x) vs2 = __hmax2(vs2, *reinterpret_cast<const __half2 *>(&vm[y][x]));
+        const float vs = __low2float(vs2);
         bool more = vs > vref;
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
-            for (int y = 0; y < 2; ++y) more |= fmaxf(s[rb][y], s[rb][y + 2]) > m[rb][y] + kLag;
+            for (int y = 0; y < 2; ++y) more |= fmaxf(s[rb][y], s[rb][y + 2]) > bound[rb][y];
         if (__any_sync(0xffffffffu, more)) {
             float big = vs;
 #pragma unroll
@@ -391,6 +514,7 @@ __global__ void __launch_bounds__(kAttnThreads) hqq_kv_attn_kernel(const Attn a)
             const float up = fmaxf(vref, __uint_as_float((__float_as_uint(big) + 0x007fffffu) & 0x7f800000u));
             const float fv = vref / up;
             vref = up;
+            vin = kWeightUnit / up;
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb) {
                 float f[2];
@@ -399,18 +523,20 @@ __global__ void __launch_bounds__(kAttnThreads) hqq_kv_attn_kernel(const Attn a)
                     float top = fmaxf(s[rb][y], s[rb][y + 2]);
 #pragma unroll
                     for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                    top = fmaxf(top, m[rb][y]);
-                    f[y] = m[rb][y] == kNegInf ? 1.0f : exp2_fast(m[rb][y] - top);  // nothing to rescale yet
+                    top = fmaxf(top * unit[rb][y], m[rb][y]);
+                    f[y] = exp2_fast(m[rb][y] - top);
                     m[rb][y] = top;
+                    bound[rb][y] = top == kLowest ? -INFINITY : (top + kLag) / unit[rb][y];
                     l[rb][y] *= f[y];
                     f[y] *= fv;
-#pragma unroll
-                    for (int x = 0; x < NG; ++x) oz[rb][y][x] *= f[y];
                 }
 #pragma unroll
-                for (int x = 0; x < VR / 2; ++x)
+                for (int y = 0; y < 4; ++y) {
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) o[rb][x][y] *= f[y & 1];
+                    for (int x = 0; x < VR / 2; ++x) o[rb][x][y] *= f[y & 1];
+#pragma unroll
+                    for (int x = 0; x < NG; ++x) oz[rb][x][y] *= f[y & 1];
+                }
             }
         }
         // ---- weights
@@ -419,139 +545,278 @@ __global__ void __launch_bounds__(kAttnThreads) hqq_kv_attn_kernel(const Attn a)
         for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-                p[rb][y] = m[rb][y & 1] == kNegInf ? 0.0f : exp2_fast(s[rb][y] - m[rb][y & 1]);
+                p[rb][y] = exp2_fast(__fmaf_rn(s[rb][y], unit[rb][y & 1], -m[rb][y & 1]));
                 l[rb][y & 1] += p[rb][y];
             }
-        const float vin = kWeightUnit / vref;
 #pragma unroll
         for (int x = 0; x < NG; ++x) {
-            const float v_a = vm[0][x].x * vin, v_b = vm[1][x].x * vin;
+            const float s_a = __low2float(*reinterpret_cast<const __half2 *>(&vm[0][x])) * vin;
+            const float s_b = __low2float(*reinterpret_cast<const __half2 *>(&vm[1][x])) * vin;
+            // a column of the tokens' zero points, alike for all 16 rows of an operand
+            const uint32_t z0 = turn(__byte_perm(vm[0][x], 0, 0x3232)), z1 = turn(__byte_perm(vm[1][x], 0, 0x3232));
             uint32_t w0[RB], w1[RB];
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb) {
-                const __half2 h0 = __floats2half2_rn(p[rb][0] * v_a, p[rb][1] * v_a);
-                const __half2 h1 = __floats2half2_rn(p[rb][2] * v_b, p[rb][3] * v_b);
-                const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-                oz[rb][0][x] = __fmaf_rn(f1.x, vm[1][x].y, __fmaf_rn(f0.x, vm[0][x].y, oz[rb][0][x]));
-                oz[rb][1][x] = __fmaf_rn(f1.y, vm[1][x].y, __fmaf_rn(f0.y, vm[0][x].y, oz[rb][1][x]));
+                const __half2 h0 = __floats2half2_rn(p[rb][0] * s_a, p[rb][1] * s_a);
+                const __half2 h1 = __floats2half2_rn(p[rb][2] * s_b, p[rb][3] * s_b);
                 w0[rb] = turn(*reinterpret_cast<const uint32_t *>(&h0));
                 w1[rb] = turn(*reinterpret_cast<const uint32_t *>(&h1));
+                mma_16816(oz[rb][x], z0, z0, z1, z1, w0[rb], w1[rb]);
             }
             // ---- O^T of this group's elements
 #pragma unroll
             for (int mb = x * (g / 16); mb < (x + 1) * (g / 16); ++mb) {
-                const uint32_t a0 = VRegs::reg(v0, v1, 2 * mb), a1 = VRegs::reg(v0, v1, 2 * mb + 1);
-                const uint32_t a2 = VRegs::reg(v2, v3, 2 * mb), a3 = VRegs::reg(v2, v3, 2 * mb + 1);
+                const uint32_t a0 = VRegs::reg(v[0], v[1], 2 * mb, sel_lo, sel_hi);
+                const uint32_t a1 = VRegs::reg(v[0], v[1], 2 * mb + 1, sel_lo, sel_hi);
+                const uint32_t a2 = VRegs::reg(v[2], v[3], 2 * mb, sel_lo, sel_hi);
+                const uint32_t a3 = VRegs::reg(v[2], v[3], 2 * mb + 1, sel_lo, sel_hi);
 #pragma unroll
                 for (int rb = 0; rb < RB; ++rb) mma_16816(o[rb][mb], a0, a1, a2, a3, w0[rb], w1[rb]);
             }
         }
+    };
+
+    int stage = 0;
+    for (int it = 0; it < steps; ++it) {
+        // block `it` has arrived for every lane, and every lane is done with block it - 1, whose
+        // stage the next copy takes
+        asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
+        __syncwarp();
+        copy(it + S::kStages - 1, stage == 0 ? S::kStages - 1 : stage - 1);
+        const uint32_t s_at = ring + stage * S::kStage;
+        if (++stage == S::kStages) stage = 0;
+        if (!(there >> (S::kStages - 1) & 1u)) continue;  // a page that is not there is not seen
+        const int t0 = (warp + it * kAttnWarps) * kBlock;
+        if (t0 >= all_lo && t0 + kBlock <= all_hi) step(s_at, t0, std::false_type{});
+        else step(s_at, t0, std::true_type{});
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the rings are free: the results take their place
 
     // ---- the warps' results meet in shared memory, in units of the values
+    float *res = reinterpret_cast<float *>(smem), *res_m = res + kAttnWarps * RU * S::kRow, *res_l = res_m + kAttnWarps * RU;
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
 #pragma unroll
-            for (int x = 4; x < 32; x *= 2) {
-                l[rb][y] += __shfl_xor_sync(0xffffffffu, l[rb][y], x);
-#pragma unroll
-                for (int z = 0; z < NG; ++z) oz[rb][y][z] += __shfl_xor_sync(0xffffffffu, oz[rb][y][z], x);
-            }
+            for (int x = 4; x < 32; x *= 2) l[rb][y] += __shfl_xor_sync(0xffffffffu, l[rb][y], x);
             if (r == 0) {
-                sm.m[warp][8 * rb + 2 * j + y] = m[rb][y];
-                sm.l[warp][8 * rb + 2 * j + y] = l[rb][y];
+                res_m[warp * RU + 8 * rb + 2 * j + y] = m[rb][y];
+                res_l[warp * RU + 8 * rb + 2 * j + y] = l[rb][y];
             }
         }
         const float vu = vref / kWeightUnit;
+        constexpr int s8 = g / 8;
 #pragma unroll
-        for (int x = 0; x < VR; ++x) {
-            constexpr int s8 = g / 8;
+        for (int x = 0; x < VR; x += 4) {  // s8 is 4 or more: four elements in a row
             const int d = x / s8 * g + r * s8 + x % s8;
-            const float out_unit = 0x1p24f / (float)(1 << VRegs::up(x));
 #pragma unroll
-            for (int y = 0; y < 2; ++y)
-                sm.o[warp][8 * rb + 2 * j + y][d] =
-                    __fmaf_rn(o[rb][x / 2][2 * (x & 1) + y], out_unit, -oz[rb][y][x / s8]) * vu;
+            for (int y = 0; y < 2; ++y) {
+                float e[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    e[i] = __fmaf_rn(o[rb][(x + i) / 2][2 * (i & 1) + y], 0x1p24f / (float)(1 << VRegs::up(x + i)),
+                                     -oz[rb][x / s8][y]) * vu;
+                *reinterpret_cast<float4 *>(res + (warp * RU + 8 * rb + 2 * j + y) * S::kRow + d) = make_float4(e[0], e[1], e[2], e[3]);
+            }
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < RU * D; e += kAttnThreads) {
-        const int rr = e / D, d = e % D, lrow = row0 + rr;
-        if (lrow >= total_rows) break;
-        float top = kNegInf;
+    for (int e = threadIdx.x; e < RU * (D / 4); e += kAttnThreads) {
+        const int rr = e / (D / 4), d = e % (D / 4) * 4;
+        if (row0 + rr > last_row) break;
+        float top = kLowest;
 #pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, sm.m[w][rr]);
-        float sum = 0.0f, acc = 0.0f;
+        for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, res_m[w * RU + rr]);
+        float sum = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int w = 0; w < kAttnWarps; ++w) {
-            const float f = sm.m[w][rr] == kNegInf ? 0.0f : exp2_fast(sm.m[w][rr] - top);
-            sum = __fmaf_rn(sm.l[w][rr], f, sum);
-            if (f > 0.0f) acc = __fmaf_rn(sm.o[w][rr][d], f, acc);
+            const float f = exp2_fast(res_m[w * RU + rr] - top);
+            sum = __fmaf_rn(res_l[w * RU + rr], f, sum);
+            const float4 v = *reinterpret_cast<const float4 *>(res + (w * RU + rr) * S::kRow + d);
+            acc[0] = __fmaf_rn(v.x, f, acc[0]);
+            acc[1] = __fmaf_rn(v.y, f, acc[1]);
+            acc[2] = __fmaf_rn(v.z, f, acc[2]);
+            acc[3] = __fmaf_rn(v.w, f, acc[3]);
         }
-        const float y = sum > 0.0f ? acc / sum : 0.0f;
-        const int64_t orow = out_row(lrow);
-        if (a.part_o) {
-            a.part_o[(part * all_rows + orow) * D + d] = y;
-            if (d == 0) a.part_lse[part * all_rows + orow] = sum > 0.0f ? top + log2f(sum) : kNegInf;
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        const float lse = sum > 0.0f ? top + log2f(sum) : -INFINITY;
+        const int64_t orow = out_row(row0 + rr);
+        if (part_o) {
+            const int64_t at = by_slot ? rr : orow;
+            *reinterpret_cast<float4 *>(part_o + at * D + d) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+            if (d == 0) part_lse[at] = lse;
         } else {
-            a.out[orow * D + d] = a.bf ? from_f32<true>(y) : from_f32<false>(y);
-            if (d == 0 && a.lse) a.lse[orow] = sum > 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : kNegInf;
+            uint16_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = a.bf ? from_f32<true>(acc[i] * inv) : from_f32<false>(acc[i] * inv);
+            *reinterpret_cast<uint2 *>(a.out + orow * D + d) =
+                make_uint2(y[0] | (uint32_t)y[1] << 16, y[2] | (uint32_t)y[3] << 16);
+            if (d == 0 && a.lse) a.lse[orow] = lse * 0.6931471805599453f;
         }
     }
 }
 
-// The chunks of one row, joined: a warp to a row, in the order of the chunks.
-template <int D>
-__global__ void __launch_bounds__(128) hqq_kv_join_kernel(const Attn a) {
-    wait_prerequisite();
+// The sequences' own tokens.  a.ctas = 0: CTA x has pair x.  Otherwise CTA x has its share of all
+// pairs' units, in order: the end of one pair, whole pairs, the beginning of another.
+template <int D, int NB, int NG, int RB>
+__global__ void __launch_bounds__(kAttnThreads, (Shape<D, NB, NG, RB>::kCtas)) hqq_kv_attn_kernel(const Attn a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ int64_t sums[kAttnWarps];
+    constexpr int RU = 8 * RB;
+    const int per = a.row_blocks * a.c.heads;  // pairs of a sequence
     const int64_t rows = (int64_t)a.batch * a.nq * a.heads;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31, parts = a.prefix_splits + a.splits;
-    if (row >= rows) return;
-    float top = kNegInf;
-    for (int p = lane; p < parts; p += 32) top = fmaxf(top, a.part_lse[p * rows + row]);
+    float *whole_o = a.part_o ? a.part_o + a.prefix_splits * rows * D : nullptr;
+    float *whole_lse = a.part_o ? a.part_lse + a.prefix_splits * rows : nullptr;
+    int b, pair;         // pair: of the sequence, row block * heads + head
+    int64_t at, left;    // the next unit of the pair; units left of this CTA's share
+    if (a.ctas == 0) {
+        b = (int)blockIdx.x / per;
+        pair = (int)blockIdx.x % per;
+        at = 0;
+        left = units_of(a, b);
+    } else {
+        const int64_t total = units_before<kAttnThreads>(a, a.batch, sums);
+        const int64_t begin = total * blockIdx.x / a.ctas;
+        left = total * (blockIdx.x + 1) / a.ctas - begin;
+        if (left == 0) return;
+        // the sequence in which the share begins: 32 at a time, by every warp alike
+        int64_t before = 0;
+        b = 0;
+        for (;;) {
+            const int mine = b + (threadIdx.x & 31);
+            const int64_t u = mine < a.batch ? units_of(a, mine) * per : 0;
+            int64_t upto = u;
+#pragma unroll
+            for (int x = 1; x < 32; x *= 2) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, upto, x);
+                if ((threadIdx.x & 31) >= x) upto += y;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, before + upto > begin);
+            if (past) {
+                const int src = __ffs(past) - 1;
+                before += __shfl_sync(0xffffffffu, upto - u, src);
+                b += src;
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, upto, 31);
+            b += 32;
+            if (b >= a.batch) return;  // not reached: the shares end with the last sequence
+        }
+        const int64_t units = units_of(a, b);
+        pair = (int)((begin - before) / units);
+        at = begin - before - pair * units;
+    }
+    for (;;) {
+        const int64_t units = units_of(a, b);
+        const int64_t take = min(units - at, left);
+        const bool whole = at == 0 && take == units;
+        float *po = whole_o, *pl = whole_lse;
+        if (!whole) {  // the first part of a pair goes to the CTA's second slot
+            const int64_t slot = (2 * (int64_t)blockIdx.x + (at == 0 ? 1 : 0)) * RU;
+            po = a.slot_o + slot * D;
+            pl = a.slot_lse + slot;
+        }
+        attend_segment<D, NB, NG, RB, false>(a, b, pair / a.c.heads * RU, pair % a.c.heads, at, at + take, po, pl, !whole, smem);
+        left -= take;
+        if (left <= 0) break;
+        at = 0;
+        if (++pair == per) {
+            pair = 0;
+            ++b;
+        }
+        __syncthreads();  // the results have been read: the rings may take their place again
+    }
+}
+
+// The prefix: CTA (x, y, z) has chunk x for block y of the batch's rows and key head z.
+template <int D, int NB, int NG, int RB>
+__global__ void __launch_bounds__(kAttnThreads, (Shape<D, NB, NG, RB>::kCtas)) hqq_kv_prefix_kernel(const Attn a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int64_t rows = (int64_t)a.batch * a.nq * a.heads, units = a.prefix_chunk / kUnit;
+    attend_segment<D, NB, NG, RB, true>(a, 0, (int)blockIdx.y * 8 * RB, (int)blockIdx.z, blockIdx.x * units,
+                                        (blockIdx.x + 1) * units, a.part_o + blockIdx.x * rows * D,
+                                        a.part_lse + blockIdx.x * rows, false, smem);
+}
+
+// Joins the parts of one row: CTA (pair, row of the pair), a warp to every kJoinWarps-th part, in
+// the order of the tokens (the prefix's chunks first).
+constexpr int kJoinWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) hqq_kv_join_kernel(const Attn a, int pair_rows) {
+    __shared__ int64_t sums[kJoinWarps];
+    __shared__ float acc_s[kJoinWarps][D], sum_s[kJoinWarps];
+    constexpr int E = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = a.row_blocks * a.c.heads;
+    const int b = (int)blockIdx.x / per, pair = (int)blockIdx.x % per, head = pair % a.c.heads;
+    const int l = pair / a.c.heads * pair_rows + (int)blockIdx.y;
+    const int64_t rows = (int64_t)a.batch * a.nq * a.heads;
+    const int64_t row = ((int64_t)b * a.nq + l / a.share) * a.heads + head * a.share + l % a.share;
+    // the CTAs that have parts of this pair
+    int c0 = 0, c1 = 0;
+    if (a.ctas > 0) {
+        const int64_t total = units_before<32 * kJoinWarps>(a, a.batch, sums);
+        const int64_t units = units_of(a, b), begin = units_before<32 * kJoinWarps>(a, b, sums) + pair * units;
+        c0 = cta_of(begin, total, a.ctas);
+        c1 = cta_of(begin + units - 1, total, a.ctas);
+    }
+    wait_prerequisite();
+    if (l >= a.nq * a.share || (c0 == c1 && a.prefix_splits == 0)) return;  // no such row, or written as a whole
+    const int parts = a.prefix_splits + c1 - c0 + 1;
+    auto find = [&](int p, const float *&o, const float *&lse) {
+        if (p < a.prefix_splits || c0 == c1) {
+            o = a.part_o + (p * rows + row) * D;
+            lse = a.part_lse + p * rows + row;
+        } else {
+            const int c = c0 + p - a.prefix_splits;
+            const int64_t at = (2 * (int64_t)c + (c == c0 ? 1 : 0)) * pair_rows + blockIdx.y;
+            o = a.slot_o + at * D;
+            lse = a.slot_lse + at;
+        }
+    };
+    const float *o, *e;
+    float top = kLowest;
+    for (int p = lane; p < parts; p += 32) {
+        find(p, o, e);
+        top = fmaxf(top, __ldcg(e));
+    }
 #pragma unroll
     for (int x = 16; x > 0; x /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    float acc[D / 32], sum = 0.0f;
+    float acc[E], sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] = 0.0f;
-    if (top > kNegInf)
-        for (int p = 0; p < parts; ++p) {
-            const float e = a.part_lse[p * rows + row];
-            if (e == kNegInf) continue;  // what lies there for this row was never written
-            const float f = exp2_fast(e - top);
-            sum += f;
-            const float *o = a.part_o + (p * rows + row) * D;
+    for (int i = 0; i < E; ++i) acc[i] = 0.0f;
+#pragma unroll 4
+    for (int p = warp; p < parts; p += kJoinWarps) {
+        find(p, o, e);
+        const float f = exp2_fast(__ldcg(e) - top);  // a part that saw nothing holds zeros
+        sum += f;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) acc[i] = __fmaf_rn(o[lane + 32 * i], f, acc[i]);
-        }
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-        const float y = sum > 0.0f ? acc[i] / sum : 0.0f;
-        a.out[row * D + lane + 32 * i] = a.bf ? from_f32<true>(y) : from_f32<false>(y);
+        for (int i = 0; i < E; ++i) acc[i] = __fmaf_rn(__ldcg(o + lane + 32 * i), f, acc[i]);
     }
-    if (a.lse && lane == 0) a.lse[row] = sum > 0.0f ? (top + log2f(sum)) * 0.6931471805599453f : kNegInf;
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc_s[warp][lane + 32 * i] = acc[i];
+    if (lane == 0) sum_s[warp] = sum;
+    __syncthreads();
+    for (int d = threadIdx.x; d < D; d += 32 * kJoinWarps) {
+        float y = 0.0f, z = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            y += acc_s[w][d];
+            z += sum_s[w];
+        }
+        y = z > 0.0f ? y / z : 0.0f;
+        a.out[row * D + d] = a.bf ? from_f32<true>(y) : from_f32<false>(y);
+        if (d == 0 && a.lse) a.lse[row] = z > 0.0f ? (top + log2f(z)) * 0.6931471805599453f : -INFINITY;
+    }
 }
-
-constexpr int64_t kSms = 148;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // rows that a CTA takes: 8, or 16 where a key head has more (and the accumulators fit)
 int rows_per_cta(int head_dim, int64_t rows) { return rows > 8 && head_dim <= 128 ? 16 : 8; }
-
-// Splits `len` tokens among about 148 * 4 CTAs for `others` independent ones: chunks of whole
-// steps of a CTA, not so short that joining costs more than it gives.
-void split_tokens(int64_t len, int64_t others, int64_t *chunk, int *splits) {
-    const int64_t step = kBlock * kAttnWarps;
-    const int64_t want = std::max<int64_t>(1, 4 * kSms / std::max<int64_t>(1, others));
-    int64_t c = ceil_div(ceil_div(std::max<int64_t>(len, 1), want), step) * step;
-    c = std::max<int64_t>(c, 2 * step);
-    *chunk = c;
-    *splits = (int)std::max<int64_t>(1, ceil_div(len, c));
-}
 
 int make_attn_plan(const hqq_kv_cache_t *cache, int64_t batch, int64_t nq, int64_t heads, int64_t max_len,
                    int64_t window, int64_t prefix_len, AttnPlan *pl) {
@@ -560,70 +825,83 @@ int make_attn_plan(const hqq_kv_cache_t *cache, int64_t batch, int64_t nq, int64
     if (rc != HQQ_OK) return rc;
     if (batch < 0 || nq < 0 || heads <= 0 || max_len < 0 || window < 0 || prefix_len < 0 || heads % c.heads)
         return HQQ_ERR_ARG;
-    // rows are counted in 31 bits, blocks of a grid's second and third dimension in 16
-    if (max_len > INT32_MAX || prefix_len > INT32_MAX || batch > 65535 / c.heads || nq > 65535 ||
+    // rows and pairs are counted in 31 bits, blocks of a grid's second and third dimension in 16
+    if (max_len > INT32_MAX || prefix_len > INT32_MAX || batch > 65535 || nq > 65535 ||
         batch * nq > INT32_MAX / heads)
         return HQQ_ERR_UNSUPPORTED;
+    *pl = AttnPlan{};
     const int64_t rows = nq * (heads / c.heads);
-    const int ru = rows_per_cta(cache->head_dim, rows);
+    const int ru = pl->pair_rows = rows_per_cta(cache->head_dim, rows);
     pl->row_blocks = (int)ceil_div(rows, ru);
-    if (pl->row_blocks > 65535) return HQQ_ERR_UNSUPPORTED;
+    const int per_sm = cache->head_dim == 256 || ru == 16 ? 2 : 4;
     int64_t span = max_len;
-    // a block of rows sees at most the window of each of its queries, and its first block's head
     if (window > 0) span = std::min<int64_t>(span, window + nq + kBlock);
-    split_tokens(span, batch * c.heads * pl->row_blocks, &pl->chunk, &pl->splits);
-    pl->prefix_splits = 0;
-    pl->prefix_chunk = 0;
-    pl->prefix_row_blocks = 0;
+    const int64_t units = std::max<int64_t>(1, ceil_div(span, kUnit)), pairs = batch * c.heads * pl->row_blocks;
+    // Pairs of at most 512 tokens have a CTA each, and no join: one launch, and no more steps in a
+    // row than the join costs.  Longer ones are shared among all SMs; a share is at least 4 units.
+    if (units > 8)
+        pl->ctas = (int)std::min<int64_t>(kSms * per_sm, std::max<int64_t>(pairs, ceil_div(pairs * units, 4)));
+    pl->slot_floats = (size_t)2 * pl->ctas * ru;
     if (prefix_len > 0) {
         const int pru = rows_per_cta(cache->head_dim, rows * batch);
         pl->prefix_row_blocks = (int)ceil_div(rows * batch, pru);
-        if (pl->prefix_row_blocks > 65535) return HQQ_ERR_UNSUPPORTED;
-        split_tokens(prefix_len, (int64_t)c.heads * pl->prefix_row_blocks, &pl->prefix_chunk, &pl->prefix_splits);
+        if (pl->prefix_row_blocks > 65535 || c.heads > 65535) return HQQ_ERR_UNSUPPORTED;
+        const int64_t want = std::max<int64_t>(1, kSms * (cache->head_dim == 256 || pru == 16 ? 2 : 4) /
+                                                      ((int64_t)c.heads * pl->prefix_row_blocks));
+        pl->prefix_chunk = std::max<int64_t>(4 * kUnit, ceil_div(ceil_div(prefix_len, want), kUnit) * kUnit);
+        pl->prefix_splits = (int)ceil_div(prefix_len, pl->prefix_chunk);
+        pl->part_floats = (size_t)(pl->prefix_splits + 1) * (size_t)(batch * nq * heads);
     }
-    const int parts = pl->splits + pl->prefix_splits;
-    pl->bytes = 0;
-    if (parts > 1) pl->bytes = (size_t)parts * (size_t)(batch * nq * heads) * (cache->head_dim + 1) * sizeof(float) + 16;
+    pl->bytes = (pl->slot_floats + pl->part_floats) * (cache->head_dim + 1) * sizeof(float);
     return HQQ_OK;
 }
 
-template <int D, int NB, int NG, int RB, bool PREFIX>
-cudaError_t launch_attn(const Attn &a, int row_blocks, cudaStream_t st) {
-    auto k = hqq_kv_attn_kernel<D, NB, NG, RB, PREFIX>;
-    constexpr int smem = (int)sizeof(Smem<D, NB, NG, RB>);
-    if constexpr (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <typename K>
+cudaError_t launch_attn(K kernel, dim3 grid, int smem, const Attn &a, cudaStream_t st) {
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    const dim3 grid(PREFIX ? a.prefix_splits : a.splits, row_blocks, PREFIX ? a.c.heads : a.batch * a.c.heads);
-    k<<<grid, kAttnThreads, smem, st>>>(a);
+    kernel<<<grid, kAttnThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
-int run_attention(const hqq_kv_cache_t *cache, Attn a, const AttnPlan &pl, cudaStream_t st) {
+int run_attention(const hqq_kv_cache_t *cache, const Attn &a, const AttnPlan &pl, cudaStream_t st) {
     if ((int64_t)a.batch * a.nq == 0) return HQQ_OK;
-    const int rows = a.nq * a.share;
-    const int rc = with_layout(*cache, [&](auto dim, auto bits, auto groups) {
+    const int64_t pairs = (int64_t)a.batch * a.row_blocks * a.c.heads;
+    if (pairs > INT32_MAX) return HQQ_ERR_UNSUPPORTED;
+    return with_layout(*cache, [&](auto dim, auto bits, auto groups) {
         constexpr int D = dim, NB = bits, NG = groups;
         constexpr int kWide = D <= 128 ? 2 : 1;
         cudaError_t e = cudaSuccess;
         if (pl.prefix_splits > 0) {
-            Attn p = a;
-            p.chunk = pl.prefix_chunk;
-            if (rows_per_cta(D, (int64_t)rows * a.batch) == 16) e = launch_attn<D, NB, NG, kWide, true>(p, pl.prefix_row_blocks, st);
-            else e = launch_attn<D, NB, NG, 1, true>(p, pl.prefix_row_blocks, st);
+            const dim3 grid(pl.prefix_splits, pl.prefix_row_blocks, a.c.heads);
+            if (rows_per_cta(D, (int64_t)a.nq * a.share * a.batch) == 16)
+                e = launch_attn(hqq_kv_prefix_kernel<D, NB, NG, kWide>, grid, Shape<D, NB, NG, kWide>::kSmem, a, st);
+            else
+                e = launch_attn(hqq_kv_prefix_kernel<D, NB, NG, 1>, grid, Shape<D, NB, NG, 1>::kSmem, a, st);
             if (e != cudaSuccess) return HQQ_ERR_CUDA;
         }
-        if (rows_per_cta(D, rows) == 16) e = launch_attn<D, NB, NG, kWide, false>(a, pl.row_blocks, st);
-        else e = launch_attn<D, NB, NG, 1, false>(a, pl.row_blocks, st);
+        const dim3 grid(a.ctas ? a.ctas : (unsigned)pairs);
+        if (pl.pair_rows == 16)
+            e = launch_attn(hqq_kv_attn_kernel<D, NB, NG, kWide>, grid, Shape<D, NB, NG, kWide>::kSmem, a, st);
+        else
+            e = launch_attn(hqq_kv_attn_kernel<D, NB, NG, 1>, grid, Shape<D, NB, NG, 1>::kSmem, a, st);
         if (e != cudaSuccess) return HQQ_ERR_CUDA;
-        if (a.part_o) {
-            const int64_t all = (int64_t)a.batch * a.nq * a.heads;
-            e = launch_pdl(hqq_kv_join_kernel<D>, (unsigned)ceil_div(all, 4), 128u, 0, st, a);
+        if (a.ctas || pl.prefix_splits) {
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)pairs, std::min(pl.pair_rows, a.nq * a.share));
+            cfg.blockDim = dim3(32 * kJoinWarps);
+            cfg.stream = st;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            e = cudaLaunchKernelEx(&cfg, hqq_kv_join_kernel<D>, a, pl.pair_rows);
         }
         return e == cudaSuccess ? HQQ_OK : HQQ_ERR_CUDA;
     });
-    return rc;
 }
 
 int check_attention(const hqq_kv_cache_t *cache, const void *q, int dtype, int64_t batch, int64_t nq, int64_t heads,
@@ -644,13 +922,21 @@ int check_attention(const hqq_kv_cache_t *cache, const void *q, int dtype, int64
 }
 
 void fill_parts(Attn *a, const AttnPlan &pl, int head_dim, void *workspace) {
-    a->chunk = pl.chunk;
-    a->splits = pl.splits;
+    a->row_blocks = pl.row_blocks;
+    a->ctas = pl.ctas;
+    a->prefix_chunk = pl.prefix_chunk;
     a->prefix_splits = pl.prefix_splits;
-    if (!pl.bytes) return;
-    const size_t rows = (size_t)(pl.splits + pl.prefix_splits) * a->batch * a->nq * a->heads;
-    a->part_o = (float *)workspace;
-    a->part_lse = a->part_o + rows * head_dim;
+    float *w = (float *)workspace;
+    if (pl.slot_floats) {
+        a->slot_o = w;
+        w += pl.slot_floats * head_dim;
+    }
+    if (pl.part_floats) {
+        a->part_o = w;
+        w += pl.part_floats * head_dim;
+    }
+    a->slot_lse = w;
+    a->part_lse = w + pl.slot_floats;
 }
 
 }  // namespace

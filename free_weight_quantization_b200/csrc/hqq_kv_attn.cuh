@@ -6,7 +6,8 @@
 namespace hqq_kv {
 
 // One attention call.  Rows are (sequence b, query i of nq, query head h); the `share` = heads /
-// kv_heads query heads of one key head, and the nq queries, read the same keys and values.
+// kv_heads query heads of one key head, and the nq queries, read the same keys and values.  A pair
+// is a block of such rows of one sequence and key head, and the tokens that it reads.
 struct Attn {
     Cache c;
     const uint16_t *q;
@@ -17,23 +18,27 @@ struct Attn {
     const int32_t *lens;               // [batch]
     int64_t max_len;
     int64_t window;                    // 0: none
-    const int32_t *prefix_pages;       // [..] of the prefix that every sequence shares
+    const int32_t *prefix_pages;       // of the prefix that every sequence shares
     int64_t prefix_len;
     float scale_log2;                  // softmax scale * log2(e)
-    int64_t chunk;                     // tokens of one split
-    int splits, prefix_splits;         // of each sequence's own tokens; of the prefix
+    int row_blocks;                    // of one sequence's rows
+    int ctas;                          // that share the sequences' own tokens evenly; 0: one to a pair
+    int64_t prefix_chunk;              // tokens of the prefix that a CTA reads
+    int prefix_splits;
     uint16_t *out;                     // [batch][nq][heads][D]
     float *lse;                        // [batch][nq][heads], null: not wanted
-    float *part_o;                     // [prefix_splits + splits][batch * nq * heads][D], null: one split
-    float *part_lse;                   // [prefix_splits + splits][batch * nq * heads], in powers of two
+    // Partial results, each normalised by itself, with their log-sum-exp in powers of two:
+    float *part_o, *part_lse;          // [prefix_splits + 1][rows][D]: the prefix's chunks, then whole
+                                       // pairs; null without a prefix
+    float *slot_o, *slot_lse;          // [2 ctas][rows of a pair][D]: pairs cut between CTAs
     bool bf;
 };
 
-// splits of the work and workspace of a call
+// how a call is divided, and its workspace
 struct AttnPlan {
-    int64_t chunk, prefix_chunk;
-    int splits, prefix_splits, row_blocks, prefix_row_blocks;
-    size_t bytes;
+    int64_t prefix_chunk;
+    int ctas, pair_rows, row_blocks, prefix_splits, prefix_row_blocks;
+    size_t part_floats, slot_floats, bytes;
 };
 
 }  // namespace hqq_kv
