@@ -196,7 +196,8 @@ struct Shape {
     static constexpr int kRow = D + 4;  // floats of a row of results: 16-byte stores, two to a bank
     static constexpr int kRing = kAttnWarps * kStages * kStage;
     static constexpr int kResult = kAttnWarps * 8 * RB * (kRow + 2) * 4;
-    static constexpr int kSmem = kRing > kResult ? kRing : kResult;
+    static constexpr int kRows = kRing > kResult ? kRing : kResult;  // the query rows lie behind
+    static constexpr int kSmem = kRows + 8 * RB * (D * 2 + NG * 4 + 12);
     static constexpr int kCtas = D == 256 || RB == 2 ? 2 : 4;
 };
 
@@ -267,121 +268,149 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
     // ---- copies: this warp's block number `it` of the segment into stage it % kStages
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (S::kStages * S::kStage);
     const int steps = (int)((to - from + kBlock - 1) / kBlock - warp + kAttnWarps - 1) / kAttnWarps;
-    const int32_t *table = PREFIX ? a.prefix_pages : a.pages + b0 * a.pages_stride;
-    const int page_mask = (1 << a.c.page_shift) - 1;
-    int page_of_lane = 0;     // the page of block number it - it % 32 + lane
-    uint32_t there = 0;       // bit i: the page of the block copied i steps ago is in the pool
-    auto copy = [&](int it, int stage) {
+    constexpr int mc = S::kMetaBytes / 16;  // chunks of metadata of each side
+    const uint8_t *k_from = a.c.codes[0] + 16 * lane, *v_from = a.c.codes[1] + 16 * lane;
+    static_assert(mc <= 32 && 2 * mc % 8 == 0, "NG is 1, 2, 4 or 8");
+    const uint8_t *m_from = (const uint8_t *)a.c.meta[lane >= mc ? 1 : 0] + 16 * (lane % mc);
+    const uint32_t k_to = ring + 16 * key_chunk(n, lane / n, lane % n);
+    const uint32_t v_to = ring + S::kCodeBytes + 16 * value_chunk(n, lane / n, lane % n);
+    const uint32_t m_to = ring + 2 * S::kCodeBytes + 16 * lane;
+    int block_of_lane = 0;    // where block number it - it % 32 + lane lies, in blocks; -1: nowhere
+    uint32_t there = 0;       // bit i: the block copied i steps ago lies in the pool
+    auto copy = [&](int it, int at) {
         there <<= 1;
         if (it < steps) {
-            const int64_t t = from + (int64_t)(warp + it * kAttnWarps) * kBlock;
             if ((it & 31) == 0) {
-                const int64_t tl = t + (int64_t)lane * kUnit;
-                page_of_lane = tl < to ? __ldg(table + (tl >> a.c.page_shift)) : -1;
-            }
-            const int page = __shfl_sync(0xffffffffu, page_of_lane, it & 31);
-            if (page >= 0 && page < a.c.pages) {
-                there |= 1u;
-                const int64_t row = row_of(a.c, page, head, (int)t & page_mask);
-                const uint32_t s = ring + stage * S::kStage;
-                const uint8_t *k = a.c.codes[0] + row * S::kRowBytes, *v = a.c.codes[1] + row * S::kRowBytes;
-#pragma unroll
-                for (int i = 0; i < (kBlock * n + 31) / 32; ++i) {
-                    const int at = lane + 32 * i;
-                    if (kBlock * n >= 32 || at < kBlock * n) {
-                        copy16(s + 16 * key_chunk(n, at / n, at % n), k + 16 * at);
-                        copy16(s + S::kCodeBytes + 16 * value_chunk(n, at / n, at % n), v + 16 * at);
-                    }
+                const int64_t t = from + (int64_t)(warp + (it + lane) * kAttnWarps) * kBlock;
+                block_of_lane = -1;
+                if (t < to) {
+                    const int32_t *table = PREFIX ? a.prefix_pages : a.pages + b0 * a.pages_stride;
+                    const int page = __ldg(table + (t >> a.c.page_shift));
+                    if (page >= 0 && page < a.c.pages)
+                        block_of_lane = (int)(row_of(a.c, page, head, (int)t & ((1 << a.c.page_shift) - 1)) / kBlock);
                 }
-                constexpr int mc = S::kMetaBytes / 16;  // chunks of metadata of each side
+            }
+            const int block = __shfl_sync(0xffffffffu, block_of_lane, it & 31);
+            if (block >= 0) {
+                there |= 1u;
+                const uint8_t *k = k_from + (int64_t)block * S::kCodeBytes, *v = v_from + (int64_t)block * S::kCodeBytes;
+                const uint8_t *m = m_from + (int64_t)block * S::kMetaBytes;
+                // 32 chunks on, a value's chunk has another place in its row (value_chunk)
+                if constexpr (n >= 2) {
 #pragma unroll
-                for (int i = 0; i < (2 * mc + 31) / 32; ++i) {
-                    const int at = lane + 32 * i;
-                    if (2 * mc % 32 == 0 || at < 2 * mc) {
-                        const int side = at >= mc ? 1 : 0;
-                        copy16(s + 2 * S::kCodeBytes + 16 * at, (const uint8_t *)(a.c.meta[side] + row * NG) + 16 * (at - side * mc));
+                    for (int i = 0; i < n / 2; ++i) {
+                        constexpr int p_step = n == 8 ? 2 : n == 16 ? 1 : 0;
+                        const int p = i * p_step & 3, turned = n == 8 ? 2 * p : n == 16 ? (p & 1) | (p & 2) << 1 : 0;
+                        copy16(k_to + at + 512 * i, k + 512 * i);
+                        copy16(((v_to - ring) ^ (16 * turned)) + ring + at + 512 * i, v + 512 * i);
                     }
+                } else if (lane < kBlock) {
+                    copy16(k_to + at, k);
+                    copy16(v_to + at, v);
+                }
+                // the metadata's 2 mc chunks, keys first: by the first lanes, or two by each lane
+                if constexpr (2 * mc <= 32) {
+                    if (2 * mc == 32 || lane < 2 * mc) copy16(m_to + at, m);
+                } else {
+                    copy16(m_to + at, m);
+                    copy16(m_to + at + 512, (const uint8_t *)a.c.meta[1] + 16 * lane + (int64_t)block * S::kMetaBytes);
                 }
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) copy(i, i);
+    for (int i = 0; i < S::kStages - 1; ++i) copy(i, i * S::kStage);
 
-    // ---- the rows of this lane: as operand column r, and as result columns 2j and 2j + 1
-    uint32_t qb[RB][KR];         // q, paired as the keys' registers are
-    float qs[RB][2][NG];         // sum of q over each group, for result columns
-    float unit[RB][2];           // what a result is to be multiplied by: powers of two out
-    int hi_[RB][2], lo_[RB][2];  // visible tokens, relative to `from`
-    int all_lo = 0, all_hi = (int)(to - from);  // tokens that every row of the block sees
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-        const int l = row0 + 8 * rb + r;
-        const bool live = l < total_rows;
-        const int lc = live ? l : row0;
+    // ---- the rows: scaled by a power of two that takes a row's largest magnitude to [2^14, 2^15)
+    // (exact, but for values 2^-20 below the largest; it makes bf16 fit fp16), into shared memory
+    // in the order of the keys' registers: lane 4r + j holds row r's share of run j
+    uint32_t *rows_q = reinterpret_cast<uint32_t *>(smem + S::kRows);          // [RB][32 lanes][KR]
+    float *rows_sum = reinterpret_cast<float *>(rows_q + RB * 32 * KR);        // [RU][NG]: sums of q
+    float *rows_unit = rows_sum + RU * NG;                                     // [RU]
+    int *rows_lo = reinterpret_cast<int *>(rows_unit + RU), *rows_hi = rows_lo + RU;  // visible tokens from `from`
+    {
+        constexpr int T = kAttnThreads / RU, E = D / T;  // threads of a row, elements of a thread
+        const int rr = threadIdx.x / T, d0 = threadIdx.x % T * E, lrow = row0 + rr;
+        const bool live = lrow < total_rows;
+        const int lc = live ? lrow : row0;
         const int b = b0 + lc / unit_rows, i = lc % unit_rows / a.share, h = head * a.share + lc % a.share;
-        const uint16_t *q = a.q + b * a.q_batch + i * a.q_token + h * a.q_head;
-        // each row is scaled by a power of two that takes its largest magnitude to [2^14, 2^15):
-        // exact, but for values 2^-20 below the largest, and it makes bf16 fit fp16
-        float big = 0.0f;
+        const uint16_t *q = a.q + b * a.q_batch + i * a.q_token + h * a.q_head + d0;
+        float x[E], big = 0.0f;
+        uint32_t raw[E / 2];
+        if (a.q_wide) {
 #pragma unroll
-        for (int x = 0; x < KR; ++x) {
-            const int e[2] = {KRegs::lo(x), KRegs::hi(x)};
-            uint32_t v[2];
+            for (int e = 0; e < E / 4; ++e) *reinterpret_cast<uint2 *>(raw + 2 * e) = __ldg((const uint2 *)q + e);
+        } else {
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const int d = e[y] / (g / 4) * g + j * (g / 4) + e[y] % (g / 4);
-                v[y] = live ? (uint32_t)__ldg(q + d) : 0u;
-                big = fmaxf(big, fabsf(a.bf ? to_f32<true>((uint16_t)v[y]) : to_f32<false>((uint16_t)v[y])));
-            }
-            qb[rb][x] = v[0] | v[1] << 16;
+            for (int e = 0; e < E / 2; ++e) raw[e] = __ldg(q + 2 * e) | (uint32_t)__ldg(q + 2 * e + 1) << 16;
         }
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const uint32_t w = live ? raw[e / 2] : 0u;
+            x[e] = a.bf ? __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16) : to_f32<false>((uint16_t)(e & 1 ? w >> 16 : w));
+            big = fmaxf(big, fabsf(x[e]));
+        }
+#pragma unroll
+        for (int y = 1; y < T; y *= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, y));
         // 2^(14 - floor(log2 big)); both it and its inverse stay normal
         const int ex = big > 0.0f ? min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 100) : 0;
         const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
-        float sum[NG];
+        float sum = 0.0f;
+        __half *to_q = reinterpret_cast<__half *>(rows_q);
 #pragma unroll
-        for (int x = 0; x < NG; ++x) sum[x] = 0.0f;
-#pragma unroll
-        for (int x = 0; x < KR; ++x) {
-            const uint32_t w = qb[rb][x];
-            float v0 = a.bf ? __uint_as_float(w << 16) : to_f32<false>((uint16_t)w);
-            float v1 = a.bf ? __uint_as_float(w & 0xffff0000u) : to_f32<false>((uint16_t)(w >> 16));
-            v0 *= up;
-            v1 *= up;
-            sum[x * NG / KR] += v0 + v1;
-            const float down = 1.0f / (float)(1 << KRegs::up(x));
-            const __half2 p = __floats2half2_rn(v0 * down, v1 * down);
-            qb[rb][x] = *reinterpret_cast<const uint32_t *>(&p);
+        for (int e = 0; e < E; ++e) {
+            x[e] *= up;
+            sum += x[e];
+            const int d = d0 + e, run = d % g / (g / 4), code = d / g * (g / 4) + d % (g / 4);
+            const int reg = code / (2 * KRegs::kSpan) * KRegs::kSpan + code % KRegs::kSpan;
+            const float down = __uint_as_float((uint32_t)(127 - code_up<NB>(reg % KRegs::kU)) << 23);
+            to_q[((rr * 4 + run) * KR + reg) * 2 + code / KRegs::kSpan % 2] = __float2half_rn(x[e] * down);
         }
 #pragma unroll
-        for (int x = 0; x < NG; ++x) {
-            sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
-            sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
-            sum[x] *= 0x1p-24f;
-        }
-        const float un = 0x1p24f / up * a.scale_log2;
-        int64_t lo, hi;
-        visible<PREFIX>(a, own_len(a, b), i, lo, hi);
-        // a row that is not there (q = 0) may see everything: its result is not written
-        const int cap = (int)(to - from);
-        const int rel_hi = live ? (int)min(max(hi - from, (int64_t)0), (int64_t)cap) : cap;
-        const int rel_lo = live ? (int)min(max(lo - from, (int64_t)0), (int64_t)cap) : 0;
-        all_hi = min(all_hi, __reduce_min_sync(0xffffffffu, rel_hi));
-        all_lo = max(all_lo, __reduce_max_sync(0xffffffffu, rel_lo));
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {  // lane 4 (2j + y) holds row 2j + y
-            const int src = 4 * (2 * j + y);
-#pragma unroll
-            for (int x = 0; x < NG; ++x) qs[rb][y][x] = __shfl_sync(0xffffffffu, sum[x], src);
-            unit[rb][y] = __shfl_sync(0xffffffffu, un, src);
-            hi_[rb][y] = __shfl_sync(0xffffffffu, rel_hi, src);
-            lo_[rb][y] = __shfl_sync(0xffffffffu, rel_lo, src);
+        for (int y = 1; y < g / E; y *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+        if (d0 % g == 0) rows_sum[rr * NG + d0 / g] = sum * 0x1p-24f;
+        if (d0 == 0) {
+            int64_t lo, hi;
+            visible<PREFIX>(a, own_len(a, b), i, lo, hi);
+            // a row that is not there (q = 0) may see everything: its result is not written
+            const int64_t cap = to - from;
+            rows_hi[rr] = live ? (int)min(max(hi - from, (int64_t)0), cap) : (int)cap;
+            rows_lo[rr] = live ? (int)min(max(lo - from, (int64_t)0), cap) : 0;
+            rows_unit[rr] = 0x1p24f / up * a.scale_log2;
         }
     }
+    __syncthreads();
+    // of this lane: as operand column r, and as result columns 2j and 2j + 1
+    uint32_t qb[RB][KR];
+    float qs[RB][2][NG];
+    float unit[RB][2];           // what a result is to be multiplied by: powers of two out
+    int hi_[RB][2], lo_[RB][2];
+    int all_lo = 0, all_hi = (int)(to - from);  // tokens that every row of the block sees
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+#pragma unroll
+        for (int x = 0; x < KR; x += 4) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(rows_q + (rb * 32 + lane) * KR + x);
+            qb[rb][x] = w.x;
+            qb[rb][x + 1] = w.y;
+            qb[rb][x + 2] = w.z;
+            qb[rb][x + 3] = w.w;
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int rr = 8 * rb + 2 * j + y;
+#pragma unroll
+            for (int x = 0; x < NG; ++x) qs[rb][y][x] = rows_sum[rr * NG + x];
+            unit[rb][y] = rows_unit[rr];
+            hi_[rb][y] = rows_hi[rr];
+            lo_[rb][y] = rows_lo[rr];
+            all_hi = min(all_hi, hi_[rb][y]);
+            all_lo = max(all_lo, lo_[rb][y]);
+        }
+    }
+    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
 
     // O^T: row r of an MMA's 16 is element 2mb of run r, row r + 8 element 2mb + 1; columns are rows
     // 2j, 2j + 1.  oz: the same for the zero points, sum of w vz (each row of the 16 alike)
@@ -576,15 +605,15 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
         }
     };
 
-    int stage = 0;
+    int stage = 0;  // byte offset of block it's stage
     for (int it = 0; it < steps; ++it) {
         // block `it` has arrived for every lane, and every lane is done with block it - 1, whose
         // stage the next copy takes
         asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
         __syncwarp();
-        copy(it + S::kStages - 1, stage == 0 ? S::kStages - 1 : stage - 1);
-        const uint32_t s_at = ring + stage * S::kStage;
-        if (++stage == S::kStages) stage = 0;
+        copy(it + S::kStages - 1, stage == 0 ? (S::kStages - 1) * S::kStage : stage - S::kStage);
+        const uint32_t s_at = ring + stage;
+        stage = stage == (S::kStages - 1) * S::kStage ? 0 : stage + S::kStage;
         if (!(there >> (S::kStages - 1) & 1u)) continue;  // a page that is not there is not seen
         const int t0 = (warp + it * kAttnWarps) * kBlock;
         if (t0 >= all_lo && t0 + kBlock <= all_hi) step(s_at, t0, std::false_type{});
@@ -965,6 +994,7 @@ extern "C" int hqq_kv_attention(const hqq_kv_cache_t *cache, const void *q, int 
     a.q_batch = q_batch_stride;
     a.q_token = q_token_stride;
     a.q_head = q_head_stride;
+    a.q_wide = aligned_to(q, 8) && (q_batch_stride | q_token_stride | q_head_stride) % 4 == 0;
     a.batch = (int)batch;
     a.nq = (int)nq;
     a.heads = (int)heads;
@@ -1002,6 +1032,7 @@ extern "C" int hqq_kv_prefix_attention(const hqq_kv_cache_t *cache, const void *
     a.q_batch = q_batch_stride;
     a.q_token = q_token_stride;
     a.q_head = q_head_stride;
+    a.q_wide = aligned_to(q, 8) && (q_batch_stride | q_token_stride | q_head_stride) % 4 == 0;
     a.batch = (int)batch;
     a.nq = (int)nq;
     a.heads = (int)heads;

@@ -12,6 +12,7 @@ struct Attn {
     Cache c;
     const uint16_t *q;
     int64_t q_batch, q_token, q_head;  // strides, in values
+    bool q_wide;                       // q can be read 8 bytes at a time
     int batch, nq, heads, share;
     const int32_t *pages;              // a row of pages_stride for each sequence
     int64_t pages_stride;

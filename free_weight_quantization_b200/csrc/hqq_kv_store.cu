@@ -30,8 +30,8 @@ int check_cache(const hqq_kv_cache_t *cache, Cache *c) {
     int shift = 0;
     while ((1 << shift) < cache->page_size && shift < 12) ++shift;
     if ((1 << shift) != cache->page_size || shift < 4 || shift > 10) return HQQ_ERR_UNSUPPORTED;
-    // rows are counted in 40 bits: byte offsets stay far inside 64
-    if (cache->kv_heads > 65535 || cache->num_pages > (int64_t(1) << 40) / cache->page_size / cache->kv_heads)
+    // blocks of 16 rows are counted in 31 bits (of the smallest rows, 320 GB for keys and values)
+    if (cache->kv_heads > 65535 || cache->num_pages > (int64_t(1) << 34) / cache->page_size / cache->kv_heads)
         return HQQ_ERR_UNSUPPORTED;
     const void *p[4] = {cache->k_codes, cache->v_codes, cache->k_meta, cache->v_meta};
     for (const void *q : p) {
