@@ -67,8 +67,10 @@ __device__ __forceinline__ void lds_piece(uint32_t *w, uint32_t at) {
     else asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
 }
 
-__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+__device__ __forceinline__ void copy16(bool wanted, uint32_t to, const void *from) {
+    asm volatile(
+        "{.reg .pred p; setp.ne.b32 p, %2, 0; @p cp.async.cg.shared.global [%0], [%1], 16;}" ::"r"(to), "l"(from),
+        "r"((int)wanted) : "memory");
 }
 
 // A 32-bit word holds codes in two halves that an operand register takes side by side.  Code u of
@@ -81,10 +83,27 @@ __host__ __device__ constexpr int code_up(int u) {
     return NB == 2 ? 6 + 2 * (u & 1) : NB == 4 ? 2 + 4 * (u & 1) : 0;
 }
 
+// a shift that stays one instruction for all the fields that are masked out of its result (left to
+// itself, the compiler masks first and then shifts each field)
+template <int BY>
+__device__ __forceinline__ uint32_t shifted(uint32_t v) {
+    uint32_t y = v;
+    if constexpr (BY > 0) asm("shl.b32 %0, %1, %2;" : "=r"(y) : "r"(v), "n"(BY));
+    if constexpr (BY < 0) asm("shr.u32 %0, %1, %2;" : "=r"(y) : "r"(v), "n"(-BY));
+    return y;
+}
+
 template <int NB>
 __device__ __forceinline__ uint32_t code_pair(uint32_t v, int h, int u) {
-    const int up = code_up<NB>(u), shift = up - (8 * h + NB * u);
-    return (shift >= 0 ? v << shift : v >> -shift) & ((((1u << NB) - 1u) * 0x00010001u) << up);
+    const uint32_t mask = (((1u << NB) - 1u) * 0x00010001u) << code_up<NB>(u);
+    if constexpr (NB == 2) {  // codes 0, 1 of a byte to bits 6, 8; codes 2, 3 too
+        const int shift = 6 - 8 * h - 4 * (u >> 1);
+        return (shift == 6 ? shifted<6>(v) : shift == 2 ? shifted<2>(v) : shift == -2 ? shifted<-2>(v) : shifted<-6>(v)) & mask;
+    } else if constexpr (NB == 4) {
+        return (h == 0 ? shifted<2>(v) : shifted<-6>(v)) & mask;
+    } else {
+        return (h == 0 ? v : shifted<-8>(v)) & mask;
+    }
 }
 
 // How the D / 4 codes of a lane's run of a key become D / 8 operand registers of two codes each:
@@ -272,55 +291,49 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
     const uint8_t *k_from = a.c.codes[0] + 16 * lane, *v_from = a.c.codes[1] + 16 * lane;
     static_assert(mc <= 32 && 2 * mc % 8 == 0, "NG is 1, 2, 4 or 8");
     const uint8_t *m_from = (const uint8_t *)a.c.meta[lane >= mc ? 1 : 0] + 16 * (lane % mc);
-    const uint32_t k_to = ring + 16 * key_chunk(n, lane / n, lane % n);
-    const uint32_t v_to = ring + S::kCodeBytes + 16 * value_chunk(n, lane / n, lane % n);
-    const uint32_t m_to = ring + 2 * S::kCodeBytes + 16 * lane;
+    const uint8_t *m2_from = (const uint8_t *)a.c.meta[1] + 16 * lane;  // where a side has 32 chunks
+    const uint32_t k_place = 16 * key_chunk(n, lane / n, lane % n);
+    const uint32_t v_place = S::kCodeBytes + 16 * value_chunk(n, lane / n, lane % n);
     int block_of_lane = 0;    // where block number it - it % 32 + lane lies, in blocks; -1: nowhere
     uint32_t there = 0;       // bit i: the block copied i steps ago lies in the pool
-    auto copy = [&](int it, int at) {
-        there <<= 1;
-        if (it < steps) {
-            if ((it & 31) == 0) {
-                const int64_t t = from + (int64_t)(warp + (it + lane) * kAttnWarps) * kBlock;
-                block_of_lane = -1;
-                if (t < to) {
-                    const int32_t *table = PREFIX ? a.prefix_pages : a.pages + b0 * a.pages_stride;
-                    const int page = __ldg(table + (t >> a.c.page_shift));
-                    if (page >= 0 && page < a.c.pages)
-                        block_of_lane = (int)(row_of(a.c, page, head, (int)t & ((1 << a.c.page_shift) - 1)) / kBlock);
-                }
-            }
-            const int block = __shfl_sync(0xffffffffu, block_of_lane, it & 31);
-            if (block >= 0) {
-                there |= 1u;
-                const uint8_t *k = k_from + (int64_t)block * S::kCodeBytes, *v = v_from + (int64_t)block * S::kCodeBytes;
-                const uint8_t *m = m_from + (int64_t)block * S::kMetaBytes;
-                // 32 chunks on, a value's chunk has another place in its row (value_chunk)
-                if constexpr (n >= 2) {
-#pragma unroll
-                    for (int i = 0; i < n / 2; ++i) {
-                        constexpr int p_step = n == 8 ? 2 : n == 16 ? 1 : 0;
-                        const int p = i * p_step & 3, turned = n == 8 ? 2 * p : n == 16 ? (p & 1) | (p & 2) << 1 : 0;
-                        copy16(k_to + at + 512 * i, k + 512 * i);
-                        copy16(((v_to - ring) ^ (16 * turned)) + ring + at + 512 * i, v + 512 * i);
-                    }
-                } else if (lane < kBlock) {
-                    copy16(k_to + at, k);
-                    copy16(v_to + at, v);
-                }
-                // the metadata's 2 mc chunks, keys first: by the first lanes, or two by each lane
-                if constexpr (2 * mc <= 32) {
-                    if (2 * mc == 32 || lane < 2 * mc) copy16(m_to + at, m);
-                } else {
-                    copy16(m_to + at, m);
-                    copy16(m_to + at + 512, (const uint8_t *)a.c.meta[1] + 16 * lane + (int64_t)block * S::kMetaBytes);
-                }
+    auto copy = [&](int it, uint32_t to_stage) {  // past the last block: nothing
+        if ((it & 31) == 0) {
+            const int64_t t = from + (int64_t)(warp + (it + lane) * kAttnWarps) * kBlock;
+            block_of_lane = -1;
+            if (t < to) {
+                const int32_t *table = PREFIX ? a.prefix_pages : a.pages + b0 * a.pages_stride;
+                const int page = __ldg(table + (t >> a.c.page_shift));
+                if (page >= 0 && page < a.c.pages)
+                    block_of_lane = (int)(row_of(a.c, page, head, (int)t & ((1 << a.c.page_shift) - 1)) / kBlock);
             }
         }
+        const int block = __shfl_sync(0xffffffffu, block_of_lane, it & 31);
+        const bool in = block >= 0;
+        there = 2 * there + (in ? 1u : 0u);
+        const uint8_t *k = k_from + (int64_t)block * S::kCodeBytes, *v = v_from + (int64_t)block * S::kCodeBytes;
+        const uint8_t *m = m_from + (int64_t)block * S::kMetaBytes;
+        const uint32_t k_to = to_stage + k_place, v_to = to_stage + v_place;
+        if constexpr (n >= 2) {
+#pragma unroll
+            for (int i = 0; i < n / 2; ++i) {
+                // 32 chunks on, a value's chunk has another place in its row (value_chunk)
+                constexpr int p_step = n == 8 ? 2 : n == 16 ? 1 : 0;
+                const int p = i * p_step & 3, turned = n == 8 ? 2 * p : n == 16 ? (p & 1) | (p & 2) << 1 : 0;
+                copy16(in, k_to + 512 * i, k + 512 * i);
+                copy16(in, turned ? to_stage + (v_place ^ (16 * turned)) + 512 * i : v_to + 512 * i, v + 512 * i);
+            }
+        } else {
+            copy16(in && lane < kBlock, k_to, k);
+            copy16(in && lane < kBlock, v_to, v);
+        }
+        // the metadata's 2 mc chunks, keys first: by the first lanes, or two by each lane
+        const uint32_t m_to = to_stage + 2 * S::kCodeBytes + 16 * lane;
+        copy16(in && lane < 2 * mc, m_to, m);
+        if constexpr (2 * mc > 32) copy16(in, m_to + 512, m2_from + (int64_t)block * S::kMetaBytes);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) copy(i, i * S::kStage);
+    for (int i = 0; i < S::kStages - 1; ++i) copy(i, ring + i * S::kStage);
 
     // ---- the rows: scaled by a power of two that takes a row's largest magnitude to [2^14, 2^15)
     // (exact, but for values 2^-20 below the largest; it makes bf16 fit fp16), into shared memory
@@ -385,8 +398,8 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
     uint32_t qb[RB][KR];
     float qs[RB][2][NG];
     float unit[RB][2];           // what a result is to be multiplied by: powers of two out
-    int hi_[RB][2], lo_[RB][2];
-    int all_lo = 0, all_hi = (int)(to - from);  // tokens that every row of the block sees
+    const int there_lo = (int)max(first - from, (int64_t)0), there_hi = (int)(to - from);  // tokens, from `from`
+    int all_lo = there_lo, all_hi = there_hi;  // those that every row of the block sees
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
 #pragma unroll
@@ -403,10 +416,8 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
 #pragma unroll
             for (int x = 0; x < NG; ++x) qs[rb][y][x] = rows_sum[rr * NG + x];
             unit[rb][y] = rows_unit[rr];
-            hi_[rb][y] = rows_hi[rr];
-            lo_[rb][y] = rows_lo[rr];
-            all_hi = min(all_hi, hi_[rb][y]);
-            all_lo = max(all_lo, lo_[rb][y]);
+            all_hi = min(all_hi, rows_hi[rr]);
+            all_lo = max(all_lo, rows_lo[rr]);
         }
     }
     all_hi = __reduce_min_sync(0xffffffffu, all_hi);
@@ -475,8 +486,8 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
             if constexpr (MASKED) {
                 // rows of a page that hold no token of this sequence hold anything: their codes are
                 // finite numbers, and their metadata are replaced by zeros
-                const int64_t t = from + t0 + r + 8 * y;
-                const bool live = t >= first && t < to;
+                const int t = t0 + r + 8 * y;
+                const bool live = t >= there_lo && t < there_hi;
 #pragma unroll
                 for (int x = 0; x < NG; ++x) {
                     km[y][x] = live ? km[y][x] : 0u;
@@ -519,8 +530,8 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
             for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    const int t = t0 + r + 8 * (y >> 1);
-                    if (t >= hi_[rb][y & 1] || t < lo_[rb][y & 1]) s[rb][y] = -INFINITY;
+                    const int t = t0 + r + 8 * (y >> 1), rr = 8 * rb + 2 * j + (y & 1);
+                    if (t >= rows_hi[rr] || t < rows_lo[rr]) s[rb][y] = -INFINITY;
                 }
         }
         // ---- a new maximum, or a larger value scale than any before: rescale
@@ -605,19 +616,19 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
         }
     };
 
-    int stage = 0;  // byte offset of block it's stage
-    for (int it = 0; it < steps; ++it) {
+    uint32_t s_at = ring;  // block it's stage
+    const uint32_t ring_last = ring + (S::kStages - 1) * S::kStage;
+    for (int it = 0, t0 = warp * kBlock; it < steps; ++it, t0 += kUnit) {
         // block `it` has arrived for every lane, and every lane is done with block it - 1, whose
         // stage the next copy takes
         asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
         __syncwarp();
-        copy(it + S::kStages - 1, stage == 0 ? (S::kStages - 1) * S::kStage : stage - S::kStage);
-        const uint32_t s_at = ring + stage;
-        stage = stage == (S::kStages - 1) * S::kStage ? 0 : stage + S::kStage;
-        if (!(there >> (S::kStages - 1) & 1u)) continue;  // a page that is not there is not seen
-        const int t0 = (warp + it * kAttnWarps) * kBlock;
-        if (t0 >= all_lo && t0 + kBlock <= all_hi) step(s_at, t0, std::false_type{});
-        else step(s_at, t0, std::true_type{});
+        copy(it + S::kStages - 1, s_at == ring ? ring_last : s_at - S::kStage);
+        if (there >> (S::kStages - 1) & 1u) {  // a page that is not there is not seen
+            if (t0 >= all_lo && t0 + kBlock <= all_hi) step(s_at, t0, std::false_type{});
+            else step(s_at, t0, std::true_type{});
+        }
+        s_at = s_at == ring_last ? ring : s_at + S::kStage;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();  // the rings are free: the results take their place
