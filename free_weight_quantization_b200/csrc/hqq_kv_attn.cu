@@ -231,36 +231,72 @@ struct Shape {
 };
 
 // units of one pair of sequence b: at least one, so that each pair has a CTA that writes its rows
-__device__ __forceinline__ int64_t units_of(const Attn &a, int b) {
+__device__ __forceinline__ uint32_t units_of(const Attn &a, int b) {
     int64_t span = own_len(a, b);
     if (a.window > 0) span = min(span, a.window + a.nq + kBlock);
-    return max((span + kUnit - 1) / kUnit, (int64_t)1);
+    return max((uint32_t)((span + kUnit - 1) / kUnit), 1u);
 }
 
-// the sum over sequences [0, n) of their pairs' units, for every thread of the CTA
-template <int THREADS>
-__device__ int64_t units_before(const Attn &a, int n, int64_t *shared) {
-    int64_t sum = 0;
-    for (int b = threadIdx.x; b < n; b += THREADS) sum += units_of(a, b);
+// CTA c's share of `total` units: the first total % ctas have one more
+struct Shares {
+    uint32_t each, more;
+    __device__ Shares(uint32_t total, uint32_t ctas) : each(total / ctas), more(total % ctas) {}
+    __device__ uint32_t begin(uint32_t c) const { return c * each + min(c, more); }
+    __device__ uint32_t owner(uint32_t x) const {  // of unit x
+        const uint32_t longer = more * (each + 1);
+        return x < longer ? x / (each + 1) : more + (x - longer) / each;
+    }
+};
+
+// Where a CTA's share begins, and what the sequences' units add up to; for all threads.
+struct Start {
+    uint32_t total, begin;  // units of all pairs; of those, the first of this CTA
+    uint32_t before;        // units of the sequences before b
+    int b;                  // the sequence that unit `begin` belongs to
+};
+
+__device__ __forceinline__ Start find_start(const Attn &a, Start *shared) {
+    __shared__ uint32_t sums[kAttnWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t per = a.row_blocks * a.c.heads;
+    const int chunk = (a.batch + kAttnThreads - 1) / kAttnThreads;  // sequences of a thread
+    const int b0 = min((int)threadIdx.x * chunk, a.batch), b1 = min(b0 + chunk, a.batch);
+    uint32_t sum = 0;
+    for (int b = b0; b < b1; ++b) sum += units_of(a, b) * per;
+    uint32_t upto = sum;
 #pragma unroll
-    for (int x = 16; x > 0; x /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    for (int x = 1; x < 32; x *= 2) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, upto, x);
+        if (lane >= x) upto += y;
+    }
+    if (lane == 31) sums[warp] = upto;
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = sum;
+    uint32_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) {
+        if (w < warp) upto += sums[w];
+        total += sums[w];
+    }
+    const uint32_t begin = Shares(total, a.ctas).begin(blockIdx.x);
+    if (begin < upto && begin >= upto - sum) {  // one thread, if the share is not empty
+        uint32_t before = upto - sum;
+        int b = b0;
+        for (;;) {
+            const uint32_t u = units_of(a, b) * per;
+            if (begin < before + u) break;
+            before += u;
+            ++b;
+        }
+        *shared = Start{total, begin, before, b};
+    }
     __syncthreads();
-    sum = 0;
-    for (int w = 0; w < THREADS / 32; ++w) sum += shared[w];
-    return sum * a.row_blocks * a.c.heads;
-}
-
-// the last CTA whose share begins at unit x or before: CTA c has [total c / ctas, total (c + 1) / ctas)
-__device__ __forceinline__ int cta_of(int64_t x, int64_t total, int ctas) {
-    return (int)(((x + 1) * ctas - 1) / total);
+    return begin < total ? *shared : Start{total, begin, total, a.batch};
 }
 
 // One segment: the blocks of tokens [first unit, last unit) of a pair, by all warps of the CTA.
 // `to_part`: where a result goes that is not the pair's whole; see the end.
 template <int D, int NB, int NG, int RB, bool PREFIX>
-__device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, int head, int64_t unit0, int64_t unit1,
+__device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, int head, uint32_t unit0, uint32_t unit1,
                                                float *part_o, float *part_lse, bool by_slot, unsigned char *smem) {
     using S = Shape<D, NB, NG, RB>;
     using KRegs = KeyRegs<D, NB, NG>;
@@ -291,8 +327,8 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
         visible<PREFIX>(a, len, last_row / a.share, lo, last);
         last = min(last, len);
     }
-    const int64_t from = (first & ~(int64_t)(kBlock - 1)) + unit0 * kUnit;
-    const int64_t to = max(min(from + (unit1 - unit0) * kUnit, last), from);
+    const int64_t from = (first & ~(int64_t)(kBlock - 1)) + (int64_t)unit0 * kUnit;
+    const int64_t to = max(min(from + (int64_t)(unit1 - unit0) * kUnit, last), from);
 
     // ---- copies: this warp's block number `it` of the segment into stage it % kStages
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (S::kStages * S::kStage);
@@ -349,7 +385,7 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
     // ---- the rows: scaled by a power of two that takes a row's largest magnitude to [2^14, 2^15)
     // (exact, but for values 2^-20 below the largest; it makes bf16 fit fp16), into shared memory
     // in the order of the keys' registers: lane 4r + j holds row r's share of run j
-    uint32_t *rows_q = reinterpret_cast<uint32_t *>(smem + S::kRows);          // [RB][32 lanes][KR]
+    uint32_t *rows_q = reinterpret_cast<uint32_t *>(smem + S::kRows);          // [RB][KR / 4][32 lanes][4]
     float *rows_sum = reinterpret_cast<float *>(rows_q + RB * 32 * KR);        // [RU][NG]: sums of q
     float *rows_unit = rows_sum + RU * NG;                                     // [RU]
     int *rows_lo = reinterpret_cast<int *>(rows_unit + RU), *rows_hi = rows_lo + RU;  // visible tokens from `from`
@@ -389,7 +425,9 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
             const int d = d0 + e, run = d % g / (g / 4), code = d / g * (g / 4) + d % (g / 4);
             const int reg = code / (2 * KRegs::kSpan) * KRegs::kSpan + code % KRegs::kSpan;
             const float down = __uint_as_float((uint32_t)(127 - code_up<NB>(reg % KRegs::kU)) << 23);
-            to_q[((rr * 4 + run) * KR + reg) * 2 + code / KRegs::kSpan % 2] = __float2half_rn(x[e] * down);
+            // in 16-byte pieces that the 32 lanes of a row block read side by side
+            const int at = (rr / 8 * (KR / 4) + reg / 4) * 128 + (rr % 8 * 4 + run) * 4 + reg % 4;
+            to_q[at * 2 + code / KRegs::kSpan % 2] = __float2half_rn(x[e] * down);
         }
 #pragma unroll
         for (int y = 1; y < g / E; y *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, y);
@@ -405,22 +443,13 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
         }
     }
     __syncthreads();
-    // of this lane: as operand column r, and as result columns 2j and 2j + 1
-    uint32_t qb[RB][KR];
+    // of this lane, as result columns 2j and 2j + 1
     float qs[RB][2][NG];
     float unit[RB][2];           // what a result is to be multiplied by: powers of two out
     const int there_lo = (int)max(first - from, (int64_t)0), there_hi = (int)(to - from);  // tokens, from `from`
     int all_lo = there_lo, all_hi = there_hi;  // those that every row of the block sees
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
-#pragma unroll
-        for (int x = 0; x < KR; x += 4) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(rows_q + (rb * 32 + lane) * KR + x);
-            qb[rb][x] = w.x;
-            qb[rb][x + 1] = w.y;
-            qb[rb][x + 2] = w.z;
-            qb[rb][x + 3] = w.w;
-        }
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
             const int rr = 8 * rb + 2 * j + y;
@@ -463,13 +492,45 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
     const uint32_t v_at[2] = {pinned(S::kCodeBytes + 16 * value_chunk(n, va, r * kValueBytes / 16) + r * kValueBytes % 16),
                               pinned(S::kCodeBytes + 16 * value_chunk(n, vb, r * kValueBytes / 16) + r * kValueBytes % 16)};
     const uint32_t sel_lo = pinned(j & 1 ? 0x1054u : 0x5410u), sel_hi = pinned(j & 1 ? 0x3276u : 0x7632u);
+    const uint32_t q_at = (uint32_t)__cvta_generic_to_shared(rows_q) + 16 * lane;
     const uint32_t m_at = pinned(2 * S::kCodeBytes + r * NG * 4);
 
-    // one block: MASKED where some row does not see all of its tokens
-    auto step = [&](uint32_t s_at, int t0, auto masked) {
-        constexpr bool MASKED = decltype(masked)::value;
-        Words<(kKeyBytes + 3) / 4> k0, k1;
+    uint32_t w[RB][NG][2], z[NG][2];  // a block's weights and its value zero points, as operands
+    // O^T += V^T W^T of the block whose stage is at `at`
+    auto values = [&](uint32_t at) {
         Words<(kValueBytes + 3) / 4> v[4];
+#pragma unroll
+        for (int i = 0; i < (kValueBytes + kValuePiece - 1) / kValuePiece; ++i)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const uint32_t from_at = at + (kValueBytes > 16 ? v_at[y & 1] ^ (uint32_t)(16 * i) : v_at[y & 1]);
+                lds_piece<kValuePiece>(v[y].w + 4 * i, from_at + (y >> 1) * 8 * S::kRowBytes);
+            }
+#pragma unroll
+        for (int x = 0; x < NG; ++x) {
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) mma_16816(oz[rb][x], z[x][0], z[x][0], z[x][1], z[x][1], w[rb][x][0], w[rb][x][1]);
+#pragma unroll
+            for (int mb = x * (g / 16); mb < (x + 1) * (g / 16); ++mb) {
+                const uint32_t a0 = VRegs::reg(v[0], v[1], 2 * mb, sel_lo, sel_hi);
+                const uint32_t a1 = VRegs::reg(v[0], v[1], 2 * mb + 1, sel_lo, sel_hi);
+                const uint32_t a2 = VRegs::reg(v[2], v[3], 2 * mb, sel_lo, sel_hi);
+                const uint32_t a3 = VRegs::reg(v[2], v[3], 2 * mb + 1, sel_lo, sel_hi);
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) mma_16816(o[rb][mb], a0, a1, a2, a3, w[rb][x][0], w[rb][x][1]);
+            }
+        }
+    };
+
+    uint32_t s_at = ring;  // block it's stage
+    const uint32_t ring_last = ring + (S::kStages - 1) * S::kStage;
+    for (int it = 0, t0 = warp * kBlock; it < steps; ++it, t0 += kUnit) {
+        // block `it` has arrived for every lane, and every lane is done with block it - 1, whose
+        // stage the next copy takes
+        asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
+        __syncwarp();
+        copy(it + S::kStages - 1, s_at == ring ? ring_last : s_at - S::kStage);
+        Words<(kKeyBytes + 3) / 4> k0, k1;
 #pragma unroll
         for (int i = 0; i < kKeyBytes / kKeyPiece; ++i) {
             // the chunks of a run lie together, or exchanged as the swizzle says
@@ -477,13 +538,6 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
             lds_piece<kKeyPiece>(k0.w + 4 * i, at);
             lds_piece<kKeyPiece>(k1.w + 4 * i, at + 8 * S::kRowBytes);
         }
-#pragma unroll
-        for (int i = 0; i < (kValueBytes + kValuePiece - 1) / kValuePiece; ++i)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const uint32_t at = s_at + (kValueBytes > 16 ? v_at[y & 1] ^ (uint32_t)(16 * i) : v_at[y & 1]);
-                lds_piece<kValuePiece>(v[y].w + 4 * i, at + (y >> 1) * 8 * S::kRowBytes);
-            }
         uint32_t km[2][NG], vm[2][NG];  // (scale, zero)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
@@ -494,20 +548,14 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
                 lds_piece<piece>(km[y] + 4 * x, at);
                 lds_piece<piece>(vm[y] + 4 * x, at + S::kMetaBytes);
             }
-            if constexpr (MASKED) {
-                // rows of a page that hold no token of this sequence hold anything: their codes are
-                // finite numbers, and their metadata are replaced by zeros
-                const int t = t0 + r + 8 * y;
-                const bool live = t >= there_lo && t < there_hi;
-#pragma unroll
-                for (int x = 0; x < NG; ++x) {
-                    km[y][x] = live ? km[y][x] : 0u;
-                    vm[y][x] = live ? vm[y][x] : 0u;
-                }
-            }
         }
-        auto meta = [](uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); };
+        auto meta = [](uint32_t m2) { return __half22float2(*reinterpret_cast<const __half2 *>(&m2)); };
 
+        uint32_t qb[RB][KR];
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+            for (int x = 0; x < KR; x += 4) lds_piece<16>(qb[rb] + x, q_at + (rb * (KR / 4) + x / 4) * 512);
         // ---- S^T: raw scores
         float s[RB][4];
 #pragma unroll
@@ -530,20 +578,31 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
             }
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-                const float2 z = meta(km[y >> 1][x]);
+                const float2 kz = meta(km[y >> 1][x]);
 #pragma unroll
                 for (int rb = 0; rb < RB; ++rb)
-                    s[rb][y] = __fmaf_rn(z.x, __fmaf_rn(-z.y, qs[rb][y & 1][x], c[rb][y]), s[rb][y]);
+                    s[rb][y] = __fmaf_rn(kz.x, __fmaf_rn(-kz.y, qs[rb][y & 1][x], c[rb][y]), s[rb][y]);
             }
         }
-        if constexpr (MASKED) {
+        // ---- where some row does not see all 16 tokens, or their page is not there.  Rows that hold
+        // no token of this sequence hold anything: their codes are finite numbers, their scores are
+        // replaced, and the values' metadata too
+        const bool in = there >> (S::kStages - 1) & 1u;
+        if (!in || t0 < all_lo || t0 + kBlock > all_hi) {
 #pragma unroll
-            for (int rb = 0; rb < RB; ++rb)
+            for (int y = 0; y < 2; ++y) {
+                const int t = t0 + r + 8 * y;
+                const bool live = in && t >= there_lo && t < there_hi;
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int t = t0 + r + 8 * (y >> 1), rr = 8 * rb + 2 * j + (y & 1);
-                    if (t >= rows_hi[rr] || t < rows_lo[rr]) s[rb][y] = -INFINITY;
-                }
+                for (int x = 0; x < NG; ++x) vm[y][x] = live ? vm[y][x] : 0u;
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int rr = 8 * rb + 2 * j + c;
+                        if (!live || t >= rows_hi[rr] || t < rows_lo[rr]) s[rb][2 * y + c] = -INFINITY;
+                    }
+            }
         }
         // ---- a new maximum, or a larger value scale than any before: rescale
         __half2 vs2 = __float2half2_rn(0.0f);
@@ -600,45 +659,19 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
                 l[rb][y & 1] += p[rb][y];
             }
 #pragma unroll
-        for (int x = 0; x < NG; ++x) {
-            const float s_a = __low2float(*reinterpret_cast<const __half2 *>(&vm[0][x])) * vin;
-            const float s_b = __low2float(*reinterpret_cast<const __half2 *>(&vm[1][x])) * vin;
-            // a column of the tokens' zero points, alike for all 16 rows of an operand
-            const uint32_t z0 = turn(__byte_perm(vm[0][x], 0, 0x3232)), z1 = turn(__byte_perm(vm[1][x], 0, 0x3232));
-            uint32_t w0[RB], w1[RB];
+        for (int x = 0; x < NG; ++x)
 #pragma unroll
-            for (int rb = 0; rb < RB; ++rb) {
-                const __half2 h0 = __floats2half2_rn(p[rb][0] * s_a, p[rb][1] * s_a);
-                const __half2 h1 = __floats2half2_rn(p[rb][2] * s_b, p[rb][3] * s_b);
-                w0[rb] = turn(*reinterpret_cast<const uint32_t *>(&h0));
-                w1[rb] = turn(*reinterpret_cast<const uint32_t *>(&h1));
-                mma_16816(oz[rb][x], z0, z0, z1, z1, w0[rb], w1[rb]);
+            for (int y = 0; y < 2; ++y) {
+                const float vw = __low2float(*reinterpret_cast<const __half2 *>(&vm[y][x])) * vin;
+                // a column of the tokens' zero points, alike for all 16 rows of an operand
+                z[x][y] = turn(__byte_perm(vm[y][x], 0, 0x3232));
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) {
+                    const __half2 h = __floats2half2_rn(p[rb][2 * y] * vw, p[rb][2 * y + 1] * vw);
+                    w[rb][x][y] = turn(*reinterpret_cast<const uint32_t *>(&h));
+                }
             }
-            // ---- O^T of this group's elements
-#pragma unroll
-            for (int mb = x * (g / 16); mb < (x + 1) * (g / 16); ++mb) {
-                const uint32_t a0 = VRegs::reg(v[0], v[1], 2 * mb, sel_lo, sel_hi);
-                const uint32_t a1 = VRegs::reg(v[0], v[1], 2 * mb + 1, sel_lo, sel_hi);
-                const uint32_t a2 = VRegs::reg(v[2], v[3], 2 * mb, sel_lo, sel_hi);
-                const uint32_t a3 = VRegs::reg(v[2], v[3], 2 * mb + 1, sel_lo, sel_hi);
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb) mma_16816(o[rb][mb], a0, a1, a2, a3, w0[rb], w1[rb]);
-            }
-        }
-    };
-
-    uint32_t s_at = ring;  // block it's stage
-    const uint32_t ring_last = ring + (S::kStages - 1) * S::kStage;
-    for (int it = 0, t0 = warp * kBlock; it < steps; ++it, t0 += kUnit) {
-        // block `it` has arrived for every lane, and every lane is done with block it - 1, whose
-        // stage the next copy takes
-        asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
-        __syncwarp();
-        copy(it + S::kStages - 1, s_at == ring ? ring_last : s_at - S::kStage);
-        if (there >> (S::kStages - 1) & 1u) {  // a page that is not there is not seen
-            if (t0 >= all_lo && t0 + kBlock <= all_hi) step(s_at, t0, std::false_type{});
-            else step(s_at, t0, std::true_type{});
-        }
+        values(s_at);
         s_at = s_at == ring_last ? ring : s_at + S::kStage;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -714,64 +747,47 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
 template <int D, int NB, int NG, int RB>
 __global__ void __launch_bounds__(kAttnThreads, (Shape<D, NB, NG, RB>::kCtas)) hqq_kv_attn_kernel(const Attn a) {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ int64_t sums[kAttnWarps];
+    __shared__ Start start_s;
     constexpr int RU = 8 * RB;
     const int per = a.row_blocks * a.c.heads;  // pairs of a sequence
     const int64_t rows = (int64_t)a.batch * a.nq * a.heads;
     float *whole_o = a.part_o ? a.part_o + a.prefix_splits * rows * D : nullptr;
     float *whole_lse = a.part_o ? a.part_lse + a.prefix_splits * rows : nullptr;
-    int b, pair;         // pair: of the sequence, row block * heads + head
-    int64_t at, left;    // the next unit of the pair; units left of this CTA's share
+    int b, pair;             // pair: of the sequence, row block * heads + head
+    uint32_t at, left;       // the next unit of the pair; units left of this CTA's share
+    uint32_t total = 0, begin = 0;
+    Cut cut{-1, 0, 0, 0};
     if (a.ctas == 0) {
         b = (int)blockIdx.x / per;
         pair = (int)blockIdx.x % per;
         at = 0;
         left = units_of(a, b);
     } else {
-        const int64_t total = units_before<kAttnThreads>(a, a.batch, sums);
-        const int64_t begin = total * blockIdx.x / a.ctas;
-        left = total * (blockIdx.x + 1) / a.ctas - begin;
-        if (left == 0) return;
-        // the sequence in which the share begins: 32 at a time, by every warp alike
-        int64_t before = 0;
-        b = 0;
-        for (;;) {
-            const int mine = b + (threadIdx.x & 31);
-            const int64_t u = mine < a.batch ? units_of(a, mine) * per : 0;
-            int64_t upto = u;
-#pragma unroll
-            for (int x = 1; x < 32; x *= 2) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, upto, x);
-                if ((threadIdx.x & 31) >= x) upto += y;
-            }
-            const unsigned past = __ballot_sync(0xffffffffu, before + upto > begin);
-            if (past) {
-                const int src = __ffs(past) - 1;
-                before += __shfl_sync(0xffffffffu, upto - u, src);
-                b += src;
-                break;
-            }
-            before += __shfl_sync(0xffffffffu, upto, 31);
-            b += 32;
-            if (b >= a.batch) return;  // not reached: the shares end with the last sequence
+        const Start start = find_start(a, &start_s);
+        total = start.total;
+        begin = start.begin;
+        left = Shares(total, a.ctas).begin(blockIdx.x + 1) - begin;
+        b = start.b;
+        if (left > 0) {
+            const uint32_t units = units_of(a, b);
+            pair = (int)((begin - start.before) / units);
+            at = begin - start.before - pair * units;
         }
-        const int64_t units = units_of(a, b);
-        pair = (int)((begin - before) / units);
-        at = begin - before - pair * units;
     }
-    for (;;) {
-        const int64_t units = units_of(a, b);
-        const int64_t take = min(units - at, left);
+    while (left > 0) {
+        const uint32_t units = units_of(a, b), take = min(units - at, left);
         const bool whole = at == 0 && take == units;
         float *po = whole_o, *pl = whole_lse;
         if (!whole) {  // the first part of a pair goes to the CTA's second slot
             const int64_t slot = (2 * (int64_t)blockIdx.x + (at == 0 ? 1 : 0)) * RU;
             po = a.slot_o + slot * D;
             pl = a.slot_lse + slot;
+            if (at == 0)
+                cut = Cut{b, pair, (int)blockIdx.x, (int)Shares(total, a.ctas).owner(begin + units - 1)};
         }
         attend_segment<D, NB, NG, RB, false>(a, b, pair / a.c.heads * RU, pair % a.c.heads, at, at + take, po, pl, !whole, smem);
         left -= take;
-        if (left <= 0) break;
+        begin += take;
         at = 0;
         if (++pair == per) {
             pair = 0;
@@ -779,44 +795,56 @@ __global__ void __launch_bounds__(kAttnThreads, (Shape<D, NB, NG, RB>::kCtas)) h
         }
         __syncthreads();  // the results have been read: the rings may take their place again
     }
+    if (a.ctas > 0 && threadIdx.x == 0) a.cuts[blockIdx.x] = cut;
 }
 
 // The prefix: CTA (x, y, z) has chunk x for block y of the batch's rows and key head z.
 template <int D, int NB, int NG, int RB>
 __global__ void __launch_bounds__(kAttnThreads, (Shape<D, NB, NG, RB>::kCtas)) hqq_kv_prefix_kernel(const Attn a) {
     extern __shared__ __align__(16) unsigned char smem[];
-    const int64_t rows = (int64_t)a.batch * a.nq * a.heads, units = a.prefix_chunk / kUnit;
+    const int64_t rows = (int64_t)a.batch * a.nq * a.heads;
+    const uint32_t units = (uint32_t)(a.prefix_chunk / kUnit);
     attend_segment<D, NB, NG, RB, true>(a, 0, (int)blockIdx.y * 8 * RB, (int)blockIdx.z, blockIdx.x * units,
                                         (blockIdx.x + 1) * units, a.part_o + blockIdx.x * rows * D,
                                         a.part_lse + blockIdx.x * rows, false, smem);
 }
 
-// Joins the parts of one row: CTA (pair, row of the pair), a warp to every kJoinWarps-th part, in
-// the order of the tokens (the prefix's chunks first).
-constexpr int kJoinWarps = 8;
+// Joins the parts of one row, a warp to every kJoinWarps-th part, in the order of the tokens (the
+// prefix's chunks first).  Without a prefix CTA (x, y) has row y of the pair that begins in CTA x's
+// share and ends in another's; with one, row y of pair x.
+constexpr int kJoinWarps = 4;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) hqq_kv_join_kernel(const Attn a, int pair_rows) {
-    __shared__ int64_t sums[kJoinWarps];
     __shared__ float acc_s[kJoinWarps][D], sum_s[kJoinWarps];
     constexpr int E = D / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per = a.row_blocks * a.c.heads;
-    const int b = (int)blockIdx.x / per, pair = (int)blockIdx.x % per, head = pair % a.c.heads;
-    const int l = pair / a.c.heads * pair_rows + (int)blockIdx.y;
-    const int64_t rows = (int64_t)a.batch * a.nq * a.heads;
-    const int64_t row = ((int64_t)b * a.nq + l / a.share) * a.heads + head * a.share + l % a.share;
-    // the CTAs that have parts of this pair
-    int c0 = 0, c1 = 0;
-    if (a.ctas > 0) {
-        const int64_t total = units_before<32 * kJoinWarps>(a, a.batch, sums);
-        const int64_t units = units_of(a, b), begin = units_before<32 * kJoinWarps>(a, b, sums) + pair * units;
-        c0 = cta_of(begin, total, a.ctas);
-        c1 = cta_of(begin + units - 1, total, a.ctas);
-    }
     wait_prerequisite();
-    if (l >= a.nq * a.share || (c0 == c1 && a.prefix_splits == 0)) return;  // no such row, or written as a whole
-    const int parts = a.prefix_splits + c1 - c0 + 1;
+    Cut cut = {(int)blockIdx.x / (a.row_blocks * a.c.heads), (int)blockIdx.x % (a.row_blocks * a.c.heads), 0, 0};
+    if (a.prefix_splits == 0) {
+        {
+            const int4 w = __ldcg((const int4 *)(a.cuts + blockIdx.x));
+            cut = Cut{w.x, w.y, w.z, w.w};
+        }
+        if (cut.b < 0) return;
+    } else {
+        // the CTAs that wrote this pair's parts, if it was cut
+        __shared__ int2 found;
+        if (threadIdx.x == 0) found = make_int2(0, 0);
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.ctas; c += 32 * kJoinWarps) {
+            const int4 w = __ldcg((const int4 *)(a.cuts + c));
+            if (w.x == cut.b && w.y == cut.pair) found = make_int2(w.z, w.w);
+        }
+        __syncthreads();
+        cut.c0 = found.x;
+        cut.c1 = found.y;
+    }
+    const int head = cut.pair % a.c.heads, l = cut.pair / a.c.heads * pair_rows + (int)blockIdx.y;
+    if (l >= a.nq * a.share) return;  // no such row
+    const int64_t rows = (int64_t)a.batch * a.nq * a.heads;
+    const int64_t row = ((int64_t)cut.b * a.nq + l / a.share) * a.heads + head * a.share + l % a.share;
+    const int c0 = cut.c0, c1 = cut.c1, parts = a.prefix_splits + c1 - c0 + 1;
     auto find = [&](int p, const float *&o, const float *&lse) {
         if (p < a.prefix_splits || c0 == c1) {
             o = a.part_o + (p * rows + row) * D;
@@ -892,6 +920,7 @@ int make_attn_plan(const hqq_kv_cache_t *cache, int64_t batch, int64_t nq, int64
     // row than the join costs.  Longer ones are shared among all SMs; a share is at least 4 units.
     if (units > 8)
         pl->ctas = (int)std::min<int64_t>(kSms * per_sm, std::max<int64_t>(pairs, ceil_div(pairs * units, 4)));
+    if (pairs > INT32_MAX / units) return HQQ_ERR_UNSUPPORTED;  // units are counted in 31 bits
     pl->slot_floats = (size_t)2 * pl->ctas * ru;
     if (prefix_len > 0) {
         const int pru = rows_per_cta(cache->head_dim, rows * batch);
@@ -903,7 +932,7 @@ int make_attn_plan(const hqq_kv_cache_t *cache, int64_t batch, int64_t nq, int64
         pl->prefix_splits = (int)ceil_div(prefix_len, pl->prefix_chunk);
         pl->part_floats = (size_t)(pl->prefix_splits + 1) * (size_t)(batch * nq * heads);
     }
-    pl->bytes = (pl->slot_floats + pl->part_floats) * (cache->head_dim + 1) * sizeof(float);
+    pl->bytes = (pl->slot_floats + pl->part_floats) * (cache->head_dim + 1) * sizeof(float) + pl->ctas * sizeof(Cut);
     return HQQ_OK;
 }
 
@@ -920,7 +949,6 @@ cudaError_t launch_attn(K kernel, dim3 grid, int smem, const Attn &a, cudaStream
 int run_attention(const hqq_kv_cache_t *cache, const Attn &a, const AttnPlan &pl, cudaStream_t st) {
     if ((int64_t)a.batch * a.nq == 0) return HQQ_OK;
     const int64_t pairs = (int64_t)a.batch * a.row_blocks * a.c.heads;
-    if (pairs > INT32_MAX) return HQQ_ERR_UNSUPPORTED;
     return with_layout(*cache, [&](auto dim, auto bits, auto groups) {
         constexpr int D = dim, NB = bits, NG = groups;
         constexpr int kWide = D <= 128 ? 2 : 1;
@@ -944,7 +972,7 @@ int run_attention(const hqq_kv_cache_t *cache, const Attn &a, const AttnPlan &pl
             attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
             attr[0].val.programmaticStreamSerializationAllowed = 1;
             cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3((unsigned)pairs, std::min(pl.pair_rows, a.nq * a.share));
+            cfg.gridDim = dim3(pl.prefix_splits ? (unsigned)pairs : (unsigned)a.ctas, std::min(pl.pair_rows, a.nq * a.share));
             cfg.blockDim = dim3(32 * kJoinWarps);
             cfg.stream = st;
             cfg.attrs = attr;
@@ -978,6 +1006,10 @@ void fill_parts(Attn *a, const AttnPlan &pl, int head_dim, void *workspace) {
     a->prefix_chunk = pl.prefix_chunk;
     a->prefix_splits = pl.prefix_splits;
     float *w = (float *)workspace;
+    if (pl.ctas) {
+        a->cuts = (Cut *)w;
+        w += pl.ctas * sizeof(Cut) / sizeof(float);
+    }
     if (pl.slot_floats) {
         a->slot_o = w;
         w += pl.slot_floats * head_dim;

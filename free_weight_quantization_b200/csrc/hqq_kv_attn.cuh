@@ -5,6 +5,10 @@
 
 namespace hqq_kv {
 
+struct __align__(16) Cut {  // a pair that is cut between CTAs c0 .. c1; b = -1: none
+    int b, pair, c0, c1;
+};
+
 // One attention call.  Rows are (sequence b, query i of nq, query head h); the `share` = heads /
 // kv_heads query heads of one key head, and the nq queries, read the same keys and values.  A pair
 // is a block of such rows of one sequence and key head, and the tokens that it reads.
@@ -32,6 +36,7 @@ struct Attn {
     float *part_o, *part_lse;          // [prefix_splits + 1][rows][D]: the prefix's chunks, then whole
                                        // pairs; null without a prefix
     float *slot_o, *slot_lse;          // [2 ctas][rows of a pair][D]: pairs cut between CTAs
+    Cut *cuts;                         // [ctas]: the pair that begins in a CTA's share and ends in another's
     bool bf;
 };
 
