@@ -230,11 +230,16 @@ struct Shape {
     static constexpr int kCtas = D == 256 || RB == 2 ? 2 : 4;
 };
 
-// units of one pair of sequence b: at least one, so that each pair has a CTA that writes its rows
+// What a pair costs beside its tokens (its queries, the filling of the rings, its results), in units:
+// pairs of short sequences would otherwise make a CTA's share longer than the others.
+constexpr uint32_t kFixed = 3;
+
+// units of one pair of sequence b: kFixed that stand for no tokens, and at least one of tokens, so
+// that each pair has a CTA that writes its rows
 __device__ __forceinline__ uint32_t units_of(const Attn &a, int b) {
     int64_t span = own_len(a, b);
     if (a.window > 0) span = min(span, a.window + a.nq + kBlock);
-    return max((uint32_t)((span + kUnit - 1) / kUnit), 1u);
+    return kFixed + max((uint32_t)((span + kUnit - 1) / kUnit), 1u);
 }
 
 // CTA c's share of `total` units: the first total % ctas have one more
@@ -330,6 +335,22 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
     const int64_t from = (first & ~(int64_t)(kBlock - 1)) + (int64_t)unit0 * kUnit;
     const int64_t to = max(min(from + (int64_t)(unit1 - unit0) * kUnit, last), from);
 
+    // ---- this thread's share of the query rows: on its way while the page table is
+    constexpr int T = kAttnThreads / RU, E = D / T;  // threads of a row, elements of a thread
+            const int rr = threadIdx.x / T, d0 = threadIdx.x % T * E, lrow = row0 + rr;
+            const bool live = lrow < total_rows;
+            const int lc = live ? lrow : row0;
+            const int b = b0 + lc / unit_rows, i = lc % unit_rows / a.share, h = head * a.share + lc % a.share;
+            const uint16_t *q = a.q + b * a.q_batch + i * a.q_token + h * a.q_head + d0;
+            uint32_t raw[E / 2];
+            if (a.q_wide) {
+#pragma unroll
+                for (int e = 0; e < E / 4; ++e) *reinterpret_cast<uint2 *>(raw + 2 * e) = __ldg((const uint2 *)q + e);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E / 2; ++e) raw[e] = __ldg(q + 2 * e) | (uint32_t)__ldg(q + 2 * e + 1) << 16;
+            }
+
     // ---- copies: this warp's block number `it` of the segment into stage it % kStages
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (S::kStages * S::kStage);
     const int steps = (int)((to - from + kBlock - 1) / kBlock - warp + kAttnWarps - 1) / kAttnWarps;
@@ -390,21 +411,7 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
     float *rows_unit = rows_sum + RU * NG;                                     // [RU]
     int *rows_lo = reinterpret_cast<int *>(rows_unit + RU), *rows_hi = rows_lo + RU;  // visible tokens from `from`
     {
-        constexpr int T = kAttnThreads / RU, E = D / T;  // threads of a row, elements of a thread
-        const int rr = threadIdx.x / T, d0 = threadIdx.x % T * E, lrow = row0 + rr;
-        const bool live = lrow < total_rows;
-        const int lc = live ? lrow : row0;
-        const int b = b0 + lc / unit_rows, i = lc % unit_rows / a.share, h = head * a.share + lc % a.share;
-        const uint16_t *q = a.q + b * a.q_batch + i * a.q_token + h * a.q_head + d0;
         float x[E], big = 0.0f;
-        uint32_t raw[E / 2];
-        if (a.q_wide) {
-#pragma unroll
-            for (int e = 0; e < E / 4; ++e) *reinterpret_cast<uint2 *>(raw + 2 * e) = __ldg((const uint2 *)q + e);
-        } else {
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) raw[e] = __ldg(q + 2 * e) | (uint32_t)__ldg(q + 2 * e + 1) << 16;
-        }
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const uint32_t w = live ? raw[e / 2] : 0u;
@@ -775,17 +782,21 @@ __global__ void __launch_bounds__(kAttnThreads, (Shape<D, NB, NG, RB>::kCtas)) h
         }
     }
     while (left > 0) {
-        const uint32_t units = units_of(a, b), take = min(units - at, left);
-        const bool whole = at == 0 && take == units;
-        float *po = whole_o, *pl = whole_lse;
-        if (!whole) {  // the first part of a pair goes to the CTA's second slot
-            const int64_t slot = (2 * (int64_t)blockIdx.x + (at == 0 ? 1 : 0)) * RU;
-            po = a.slot_o + slot * D;
-            pl = a.slot_lse + slot;
-            if (at == 0)
-                cut = Cut{b, pair, (int)blockIdx.x, (int)Shares(total, a.ctas).owner(begin + units - 1)};
+        const uint32_t units = units_of(a, b), take = min(units - at, left), end = at + take;
+        if (end > kFixed) {
+            const bool top = at <= kFixed, whole = top && end == units;  // top: the pair's first tokens
+            float *po = whole_o, *pl = whole_lse;
+            if (!whole) {  // the first part of a pair goes to the CTA's second slot
+                const int64_t slot = (2 * (int64_t)blockIdx.x + (top ? 1 : 0)) * RU;
+                po = a.slot_o + slot * D;
+                pl = a.slot_lse + slot;
+                if (top)
+                    cut = Cut{b, pair, (int)blockIdx.x, (int)Shares(total, a.ctas).owner(begin + units - at - 1)};
+            }
+            attend_segment<D, NB, NG, RB, false>(a, b, pair / a.c.heads * RU, pair % a.c.heads, top ? 0 : at - kFixed,
+                                                 end - kFixed, po, pl, !whole, smem);
+            __syncthreads();  // the results have been read: the rings may take their place again
         }
-        attend_segment<D, NB, NG, RB, false>(a, b, pair / a.c.heads * RU, pair % a.c.heads, at, at + take, po, pl, !whole, smem);
         left -= take;
         begin += take;
         at = 0;
@@ -793,7 +804,6 @@ __global__ void __launch_bounds__(kAttnThreads, (Shape<D, NB, NG, RB>::kCtas)) h
             pair = 0;
             ++b;
         }
-        __syncthreads();  // the results have been read: the rings may take their place again
     }
     if (a.ctas > 0 && threadIdx.x == 0) a.cuts[blockIdx.x] = cut;
 }
@@ -915,10 +925,10 @@ int make_attn_plan(const hqq_kv_cache_t *cache, int64_t batch, int64_t nq, int64
     const int per_sm = cache->head_dim == 256 || ru == 16 ? 2 : 4;
     int64_t span = max_len;
     if (window > 0) span = std::min<int64_t>(span, window + nq + kBlock);
-    const int64_t units = std::max<int64_t>(1, ceil_div(span, kUnit)), pairs = batch * c.heads * pl->row_blocks;
+    const int64_t units = kFixed + std::max<int64_t>(1, ceil_div(span, kUnit)), pairs = batch * c.heads * pl->row_blocks;
     // Pairs of at most 512 tokens have a CTA each, and no join: one launch, and no more steps in a
     // row than the join costs.  Longer ones are shared among all SMs; a share is at least 4 units.
-    if (units > 8)
+    if (units > kFixed + 8)
         pl->ctas = (int)std::min<int64_t>(kSms * per_sm, std::max<int64_t>(pairs, ceil_div(pairs * units, 4)));
     if (pairs > INT32_MAX / units) return HQQ_ERR_UNSUPPORTED;  // units are counted in 31 bits
     pl->slot_floats = (size_t)2 * pl->ctas * ru;
