@@ -15,11 +15,11 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 UNITS = ["hqq_abi.cu", "hqq_stream.cu", "hqq_tile_a.cu", "hqq_tile_b.cu", "hqq_dequant.cu",
-         "hqq_gemm.cu", "hqq_kv_store.cu", "hqq_kv_attn.cu"]
+         "hqq_gemm.cu", "hqq_kv_store.cu", "hqq_kv_attn.cu", "hqq_kv_prefix.cu"]
 SRCS = [os.path.join(CSRC, u) for u in UNITS]
 HDRS = [os.path.join(ROOT, "include", "hqq_b200.h"), os.path.join(CSRC, "hqq_common.cuh"),
         os.path.join(CSRC, "hqq_tile.cuh"), os.path.join(CSRC, "hqq_kv.cuh"),
-        os.path.join(CSRC, "hqq_kv_attn.cuh")]
+        os.path.join(CSRC, "hqq_kv_attn.cuh"), os.path.join(CSRC, "hqq_umma.cuh")]
 LIB = os.path.join(HERE, "libhqq_b200.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 

@@ -40,6 +40,7 @@
 #include <mutex>
 
 #include "hqq_common.cuh"
+#include "hqq_umma.cuh"
 
 namespace {
 
@@ -57,7 +58,6 @@ constexpr int kGmLag = 4;          // A buffers (tensor memory): tiles dequantiz
 // TMA row request carries 128 bytes, and the 128-byte swizzle spreads a warp's reads over the banks
 constexpr int kGmChunkRow = 128;
 constexpr int kGmChunkBytes = kGmM * kGmChunkRow;
-constexpr uint32_t kGmWaitLimit = 1u << 20;
 
 // shared-memory layout of a CTA (offsets from a 1024-byte aligned base): two code-chunk buffers,
 // S X slots, the scale/zero table, the mbarriers and the tensor-memory address
@@ -74,52 +74,9 @@ struct GemmLayout {
     }
 };
 
-// tcgen05 shared-memory matrix descriptor: start address, leading-dimension byte offset,
-// stride byte offset, all in 16-byte units; descriptor version 1; layout type (0: no swizzle,
-// 2: 128-byte swizzle)
-__device__ __forceinline__ uint64_t umma_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)layout << 61);
-}
-
 // instruction descriptor of kind::f16: D binary32, A and B fp16, both K-major, M = 128, N = np
 __host__ __device__ constexpr uint32_t umma_idesc_f16(int np) {
     return (1u << 4) | ((uint32_t)(np >> 3) << 17) | ((uint32_t)(kGmM >> 4) << 24);
-}
-
-__device__ __forceinline__ void mbar_init(uint32_t addr, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(addr), "r"(count) : "memory");
-}
-
-// one test of the phase with the given parity
-__device__ __forceinline__ bool mbar_try(uint32_t addr, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred P1;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 P1, [%1], %2;\n\t"
-        "selp.b32 %0, 1, 0, P1;\n\t}"
-        : "=r"(ok)
-        : "r"(addr), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// bounded wait for the phase with the given parity, out of line: the hot loops only pay for it
-// when the first test fails; false if the phase did not complete in time
-__device__ __noinline__ bool mbar_wait_slow(uint32_t addr, uint32_t parity) {
-    for (uint32_t i = 0; i < kGmWaitLimit; ++i) {
-        if (mbar_try(addr, parity)) return true;
-        if (i >= 4) __nanosleep(64);  // a waiting warp leaves the issue slots to the working ones
-    }
-    return false;
-}
-
-__device__ __forceinline__ bool mbar_wait(uint32_t addr, uint32_t parity) {
-    return mbar_try(addr, parity) || mbar_wait_slow(addr, parity);
-}
-
-__device__ __forceinline__ void mbar_arrive(uint32_t addr) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
 __device__ __forceinline__ void mbar_expect_tx(uint32_t addr, uint32_t bytes) {
@@ -131,10 +88,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
         ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(mbar) : "memory");
-}
-
-__device__ __forceinline__ void umma_commit(uint32_t mbar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mbar) : "memory");
 }
 
 // The 8 codes of one 16-byte piece of a W_hat row (k8 chunk), dequantized exactly as

@@ -47,12 +47,6 @@ constexpr int kAttnWarps = 4, kAttnThreads = 32 * kAttnWarps;
 constexpr int kBlock = 16;                      // tokens of one step of a warp
 constexpr int kUnit = kBlock * kAttnWarps;       // of one step of a CTA
 constexpr int kSms = 148;
-constexpr float kLowest = -1e30f;  // a maximum before any score
-// The running maximum may lag behind by this many powers of two before the sums are rescaled:
-// weights stay below 2^8 of what they are relative to.  w is kept within fp16 by 2^6 * 2^8 < 65504.
-constexpr float kLag = 8.0f;
-constexpr float kWeightUnit = 64.0f;
-
 template <int N>
 struct Words {
     uint32_t w[N];
@@ -71,39 +65,6 @@ __device__ __forceinline__ void copy16(bool wanted, uint32_t to, const void *fro
     asm volatile(
         "{.reg .pred p; setp.ne.b32 p, %2, 0; @p cp.async.cg.shared.global [%0], [%1], 16;}" ::"r"(to), "l"(from),
         "r"((int)wanted) : "memory");
-}
-
-// A 32-bit word holds codes in two halves that an operand register takes side by side.  Code u of
-// byte h of the halves is brought to bit up(u): as high as it can be below the fp16 exponent at
-// one shift for two codes, because the tensor cores align a subnormal number as if its leading
-// bit were at the top, and what they drop is relative to that.  (Measured on scores, relative
-// error of the log-sum-exp at 2 / 4 bits: 5e-6 / 1e-6 with the codes where they lie.)
-template <int NB>
-__host__ __device__ constexpr int code_up(int u) {
-    return NB == 2 ? 6 + 2 * (u & 1) : NB == 4 ? 2 + 4 * (u & 1) : 0;
-}
-
-// a shift that stays one instruction for all the fields that are masked out of its result (left to
-// itself, the compiler masks first and then shifts each field)
-template <int BY>
-__device__ __forceinline__ uint32_t shifted(uint32_t v) {
-    uint32_t y = v;
-    if constexpr (BY > 0) asm("shl.b32 %0, %1, %2;" : "=r"(y) : "r"(v), "n"(BY));
-    if constexpr (BY < 0) asm("shr.u32 %0, %1, %2;" : "=r"(y) : "r"(v), "n"(-BY));
-    return y;
-}
-
-template <int NB>
-__device__ __forceinline__ uint32_t code_pair(uint32_t v, int h, int u) {
-    const uint32_t mask = (((1u << NB) - 1u) * 0x00010001u) << code_up<NB>(u);
-    if constexpr (NB == 2) {  // codes 0, 1 of a byte to bits 6, 8; codes 2, 3 too
-        const int shift = 6 - 8 * h - 4 * (u >> 1);
-        return (shift == 6 ? shifted<6>(v) : shift == 2 ? shifted<2>(v) : shift == -2 ? shifted<-2>(v) : shifted<-6>(v)) & mask;
-    } else if constexpr (NB == 4) {
-        return (h == 0 ? shifted<2>(v) : shifted<-6>(v)) & mask;
-    } else {
-        return (h == 0 ? v : shifted<-8>(v)) & mask;
-    }
 }
 
 // How the D / 4 codes of a lane's run of a key become D / 8 operand registers of two codes each:
@@ -186,33 +147,7 @@ __device__ __forceinline__ const T *pinned(const T *p) {
     return (const T *)((uint64_t)pinned((uint32_t)(v >> 32)) << 32 | pinned((uint32_t)v));
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // Rows of one key head are numbered l = (b - b0) * nq * share + i * share + (h - head * share).
-
-// a sequence's own tokens that count
-__device__ __forceinline__ int64_t own_len(const Attn &a, int b) {
-    const int64_t n = __ldg(a.lens + b);
-    return n < 0 ? 0 : n > a.max_len ? a.max_len : n;
-}
-
-// tokens [lo, hi) of the sequence (or of the prefix) that query i of sequence b sees
-template <bool PREFIX>
-__device__ __forceinline__ void visible(const Attn &a, int64_t len, int i, int64_t &lo, int64_t &hi) {
-    const int64_t end = len - a.nq + 1 + i;  // among the sequence's own tokens
-    lo = 0;
-    if constexpr (PREFIX) {
-        hi = end < 0 ? a.prefix_len + end : a.prefix_len;
-    } else {
-        hi = end;
-        if (a.window > 0 && end > a.window) lo = end - a.window;
-    }
-    if (hi < 0) hi = 0;
-}
 
 // What a kernel of this layout keeps in shared memory and how many of its CTAs an SM holds.
 template <int D, int NB, int NG, int RB>
@@ -902,6 +837,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) hqq_kv_join_kernel(const Attn
     }
 }
 
+// rows of a key head over the whole batch above which the prefix goes to the tensor-core kernel
+constexpr int kTcMinRows = 32;
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // rows that a CTA takes: 8, or 16 where a key head has more (and the accumulators fit)
@@ -932,13 +870,21 @@ int make_attn_plan(const hqq_kv_cache_t *cache, int64_t batch, int64_t nq, int64
         pl->ctas = (int)std::min<int64_t>(kSms * per_sm, std::max<int64_t>(pairs, ceil_div(pairs * units, 4)));
     if (pairs > INT32_MAX / units) return HQQ_ERR_UNSUPPORTED;  // units are counted in 31 bits
     pl->slot_floats = (size_t)2 * pl->ctas * ru;
-    if (prefix_len > 0) {
+    pl->prefix_tc = prefix_len > 0 && rows * batch > kTcMinRows && prefix_tc_layout(*cache);
+    if (pl->prefix_tc) {
+        pl->prefix_row_blocks = (int)ceil_div(rows * batch, kTcRows);
+        if (pl->prefix_row_blocks > 65535 || c.heads > 65535) return HQQ_ERR_UNSUPPORTED;
+        const int64_t want = std::max<int64_t>(1, 2 * kSms / ((int64_t)c.heads * pl->prefix_row_blocks));
+        pl->prefix_chunk = std::max<int64_t>(4 * kTcTokens, ceil_div(ceil_div(prefix_len, want), kTcTokens) * kTcTokens);
+    } else if (prefix_len > 0) {
         const int pru = rows_per_cta(cache->head_dim, rows * batch);
         pl->prefix_row_blocks = (int)ceil_div(rows * batch, pru);
         if (pl->prefix_row_blocks > 65535 || c.heads > 65535) return HQQ_ERR_UNSUPPORTED;
         const int64_t want = std::max<int64_t>(1, kSms * (cache->head_dim == 256 || pru == 16 ? 2 : 4) /
                                                       ((int64_t)c.heads * pl->prefix_row_blocks));
         pl->prefix_chunk = std::max<int64_t>(4 * kUnit, ceil_div(ceil_div(prefix_len, want), kUnit) * kUnit);
+    }
+    if (prefix_len > 0) {
         pl->prefix_splits = (int)ceil_div(prefix_len, pl->prefix_chunk);
         pl->part_floats = (size_t)(pl->prefix_splits + 1) * (size_t)(batch * nq * heads);
     }
@@ -965,7 +911,9 @@ int run_attention(const hqq_kv_cache_t *cache, const Attn &a, const AttnPlan &pl
         cudaError_t e = cudaSuccess;
         if (pl.prefix_splits > 0) {
             const dim3 grid(pl.prefix_splits, pl.prefix_row_blocks, a.c.heads);
-            if (rows_per_cta(D, (int64_t)a.nq * a.share * a.batch) == 16)
+            if (pl.prefix_tc)
+                e = launch_prefix_tc(*cache, a, pl.prefix_row_blocks, st);
+            else if (rows_per_cta(D, (int64_t)a.nq * a.share * a.batch) == 16)
                 e = launch_attn(hqq_kv_prefix_kernel<D, NB, NG, kWide>, grid, Shape<D, NB, NG, kWide>::kSmem, a, st);
             else
                 e = launch_attn(hqq_kv_prefix_kernel<D, NB, NG, 1>, grid, Shape<D, NB, NG, 1>::kSmem, a, st);

@@ -44,7 +44,78 @@ struct Attn {
 struct AttnPlan {
     int64_t prefix_chunk;
     int ctas, pair_rows, row_blocks, prefix_splits, prefix_row_blocks;
+    bool prefix_tc;  // the prefix by hqq_kv_prefix_tc_kernel
     size_t part_floats, slot_floats, bytes;
 };
+
+constexpr float kLowest = -1e30f;  // a maximum before any score
+// The running maximum may lag behind by this many powers of two before the sums are rescaled:
+// weights stay below 2^8 of what they are relative to.  w is kept within fp16 by 2^6 * 2^8 < 65504.
+constexpr float kLag = 8.0f;
+constexpr float kWeightUnit = 64.0f;
+
+// A 32-bit word holds codes in two halves that an operand register takes side by side.  Code u of
+// byte h of the halves is brought to bit up(u): as high as it can be below the fp16 exponent at
+// one shift for two codes, because the tensor cores align a subnormal number as if its leading
+// bit were at the top, and what they drop is relative to that.  (Measured on scores, relative
+// error of the log-sum-exp at 2 / 4 bits: 5e-6 / 1e-6 with the codes where they lie.)
+template <int NB>
+__host__ __device__ constexpr int code_up(int u) {
+    return NB == 2 ? 6 + 2 * (u & 1) : NB == 4 ? 2 + 4 * (u & 1) : 0;
+}
+
+// a shift that stays one instruction for all the fields that are masked out of its result (left to
+// itself, the compiler masks first and then shifts each field)
+template <int BY>
+__device__ __forceinline__ uint32_t shifted(uint32_t v) {
+    uint32_t y = v;
+    if constexpr (BY > 0) asm("shl.b32 %0, %1, %2;" : "=r"(y) : "r"(v), "n"(BY));
+    if constexpr (BY < 0) asm("shr.u32 %0, %1, %2;" : "=r"(y) : "r"(v), "n"(-BY));
+    return y;
+}
+
+template <int NB>
+__device__ __forceinline__ uint32_t code_pair(uint32_t v, int h, int u) {
+    const uint32_t mask = (((1u << NB) - 1u) * 0x00010001u) << code_up<NB>(u);
+    if constexpr (NB == 2) {  // codes 0, 1 of a byte to bits 6, 8; codes 2, 3 too
+        const int shift = 6 - 8 * h - 4 * (u >> 1);
+        return (shift == 6 ? shifted<6>(v) : shift == 2 ? shifted<2>(v) : shift == -2 ? shifted<-2>(v) : shifted<-6>(v)) & mask;
+    } else if constexpr (NB == 4) {
+        return (h == 0 ? shifted<2>(v) : shifted<-6>(v)) & mask;
+    } else {
+        return (h == 0 ? v : shifted<-8>(v)) & mask;
+    }
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// a sequence's own tokens that count
+__device__ __forceinline__ int64_t own_len(const Attn &a, int b) {
+    const int64_t n = __ldg(a.lens + b);
+    return n < 0 ? 0 : n > a.max_len ? a.max_len : n;
+}
+
+// tokens [lo, hi) of the sequence (or of the prefix) that query i of sequence b sees
+template <bool PREFIX>
+__device__ __forceinline__ void visible(const Attn &a, int64_t len, int i, int64_t &lo, int64_t &hi) {
+    const int64_t end = len - a.nq + 1 + i;  // among the sequence's own tokens
+    lo = 0;
+    if constexpr (PREFIX) {
+        hi = end < 0 ? a.prefix_len + end : a.prefix_len;
+    } else {
+        hi = end;
+        if (a.window > 0 && end > a.window) lo = end - a.window;
+    }
+    if (hi < 0) hi = 0;
+}
+
+// the tensor-core prefix (hqq_kv_prefix.cu): its layouts, the rows of a CTA, tokens of a tile
+constexpr int kTcRows = 128, kTcTokens = 64;
+inline bool prefix_tc_layout(const hqq_kv_cache_t &c) { return c.head_dim <= 128 && c.group_size >= 64; }
+cudaError_t launch_prefix_tc(const hqq_kv_cache_t &cache, const Attn &a, int row_tiles, cudaStream_t st);
 
 }  // namespace hqq_kv
