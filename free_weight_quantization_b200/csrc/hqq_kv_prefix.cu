@@ -148,6 +148,15 @@ __device__ __forceinline__ bool wait_for(uint32_t addr, uint32_t parity) {
     return false;
 }
 
+// one lane of a converged warp.  The products' descriptors live in uniform registers: behind this
+// the compiler knows that a single lane issues them, behind `lane == 0` it does not, and moves
+// each operand over on its own
+__device__ __forceinline__ bool elected() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred P1;\n\telect.sync _|P1, 0xffffffff;\n\tselp.b32 %0, 1, 0, P1;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // D binary32, A and B fp16, M = 128; `along_n`: B's elements lie along N
 __host__ __device__ constexpr uint32_t tc_idesc(int n, bool along_n) {
     return (1u << 4) | (along_n ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTcRows >> 4) << 24);
@@ -160,7 +169,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile uint32_t failed;  // a wait ran out somewhere
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, role = warp >> 2;  // 0 softmax, 1 producers, 2 issue
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), role = warp >> 2;  // 0 softmax, 1 producers, 2 issue
     const int split = blockIdx.x, row0 = (int)blockIdx.y * kTcRows, head = blockIdx.z;
     const uint32_t base = ((uint32_t)__cvta_generic_to_shared(smem_raw) + 1023u) & ~1023u;
     const uint32_t bars = base + S::kBars;
@@ -337,7 +346,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
         if (!ok) failed = 1;
     } else if (role == 2) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-        if (warp == 8 && lane == 0) {
+        if (warp == 8 && elected()) {
             constexpr uint32_t s_idesc = tc_idesc(kTcTokens, false), o_idesc = tc_idesc(g, true);
             for (int i = 0; i < tiles; ++i) {
                 const int st = i & 1;
