@@ -3,22 +3,28 @@
 //
 // A CTA has 128 query rows of one key head (of any sequences) and a chunk of the prefix, which it
 // takes in tiles of 64 tokens:
-//     S_g = Q_g A_g^T            for each group g of the keys' elements; A: the codes as they are
-//     s   = sum_g ks_g (S_g - kz_g sum Q_g),   p = exp2(s - m)
-//     O_g += (p vs_g) (C_g - vz_g)
-// As in hqq_kv_attn.cu the keys' codes are exact (fp16 subnormals, their power of two in Q), scales
-// stay in binary32 outside the products, and p vs is rounded to fp16 once; C - vz is rounded to
-// fp16 (exact where the zero point has few bits), which saves the zero points' sum over tokens.
+//     S_g = Q_g (A_g - kz_g)^T   for each group g of the keys' elements; A: the codes as they are
+//     s   = sum_g ks_g S_g,   p = exp2(s - m),   O += p V
+// As in hqq_kv_attn.cu the keys' codes are exact (fp16 subnormals, their power of two in Q) and
+// their scales stay in binary32 outside the product; the zero points are one more step of it, 16
+// wide: the row's -sum Q_g in two fp16 parts against (kz, kz).  The values are computed in binary32,
+// (c - vz) vs, relative to a power of two at the group's largest scale so far, and rounded to fp16
+// once, as the weights p are.
+// What a row needs of each token is thus NG floats; all of it (ks, kz, vs of each group) would be
+// read by 128 rows 24 bytes a token, and shared memory gives 128 bytes a cycle: 1500 cycles for a
+// tile whose products take 600.
 //
-// Twelve warps, two CTAs on an SM:
+// Sixteen warps, two CTAs on an SM:
 //   * four producer warps turn the codes of a tile into operands in shared memory (128-byte
 //     swizzle; keys K-major, values with the elements along the rows), two stages, and the
 //     metadata into binary32 arrays;
 //   * one lane issues the tcgen05.mma: S_g (128 x 64, binary32, tensor memory), then O_g with the
 //     weights as the A operand in tensor memory, where they take the place of S;
-//   * four softmax warps: a thread has one row, reads its scores from tensor memory, keeps the
-//     running maximum and sum, and writes the weights.  O is rescaled in tensor memory only when
-//     the maximum has grown by more than 2^8, or a larger value scale appears.
+//   * eight softmax warps: two threads have a row, 32 tokens of a tile each; they read their
+//     scores from tensor memory, keep a common running maximum and a sum each, and write the
+//     weights.  O is rescaled in tensor memory only when the maximum has grown by more than 2^8, or
+//     a larger value scale appears.  (With one thread a row, four warps, the turn of a tile took
+//     5500 cycles, 3300 of them here: a warp alone on its scheduler waits for itself.)
 // The two CTAs of an SM cover each other's turns: while one's scores are in its softmax warps the
 // other's products run.
 //
@@ -33,18 +39,27 @@ namespace {
 
 using namespace hqq_kv;
 
-constexpr int kTcThreads = 384;
-// registers of a thread: 80 at launch (two CTAs of 384), divided so that the sum is the same
-constexpr int kTcLaunchRegs = 80, kSoftmaxRegs = 144, kProducerRegs = 72, kIssueRegs = 24;
-static_assert(kSoftmaxRegs + kProducerRegs + kIssueRegs <= 3 * kTcLaunchRegs, "setmaxnreg draws on the launch's registers");
+constexpr int kTcThreads = 512, kSoftmaxThreads = 256;
+// registers of a thread: 64 at launch (two CTAs of 512), divided so that the sum is the same
+constexpr int kTcLaunchRegs = 64, kSoftmaxRegs = 80, kProducerRegs = 72, kIssueRegs = 24;
+static_assert(2 * kSoftmaxRegs + kProducerRegs + kIssueRegs <= 4 * kTcLaunchRegs, "setmaxnreg draws on the launch's registers");
+static_assert(kSoftmaxRegs >= kTcLaunchRegs && kProducerRegs >= kTcLaunchRegs && kIssueRegs <= kTcLaunchRegs,
+              "an increase to fewer registers, or a decrease to more, is an illegal instruction");
 
 template <int D, int NG>
 struct TcShape {
     static constexpr int kBlocks = D / 64;  // of 64 elements: 128 bytes, a row of the swizzle
     static constexpr int kQ = kBlocks * kTcRows * 128, kTile = kBlocks * kTcTokens * 128;
-    static constexpr int kMeta = 3 * NG * kTcTokens * 4 + 16;  // ks, -kz, vs; valid[2], largest vs[2]
-    static constexpr int kStage0 = kQ, kMeta0 = kQ + 4 * kTile, kBars = kMeta0 + 2 * kMeta;
-    static constexpr int kSmem = kBars + 64 + 1024;            // + alignment slack
+    // the zero points' step: of its 16 columns 8 are held, two of them not zero, and 8 lie in one piece
+    // of zeros for all
+    static constexpr int kZqG = kTcRows * 16, kZkG = kTcTokens * 16, kZero = kZqG;
+    static constexpr int kMeta = NG * kTcTokens * 4 + 16;  // ks; valid[2], the values' unit of each group
+    static constexpr int kZq0 = kQ, kStage0 = kZq0 + NG * kZqG, kZk0 = kStage0 + 4 * kTile, kZero0 = kZk0 + 2 * NG * kZkG;
+    static constexpr int kMeta0 = kZero0 + kZero;
+    static constexpr int kTops0 = kMeta0 + 2 * kMeta;      // [4 warps][NG]: largest value scales
+    static constexpr int kBars = kTops0 + 16 * NG;
+    static constexpr int kRow0 = kBars + 64;                   // [2][128] floats: what a row's two threads exchange
+    static constexpr int kSmem = kRow0 + 8 * kTcRows + 1024;   // + alignment slack
     static constexpr int kOCol = NG * kTcTokens;               // O behind S in tensor memory
     static constexpr int kCols = kOCol + D <= 128 ? 128 : 256;
 };
@@ -72,29 +87,42 @@ __device__ __forceinline__ uint4 key_chunk8(const uint32_t *w) {
     }
 }
 
-// the field of NB bits at bit `at` of both halves of v, less z: with the exponent of 1024 put
-// above it a field is 1024 + code * 2^at, and the code is exact after one multiply-add
+// The same 8 codes in the same places as values: (code - zero) * scale, rounded once.  A code
+// becomes a binary32 number by one byte permute: under the exponent of 128 (2^15 for 8-bit codes)
+// its byte counts whole numbers, and the same number is added to the zero point beforehand, which
+// moves it by at most 2^-17 (2^-9 of 255) of a step.
 template <int NB>
-__device__ __forceinline__ uint32_t field_less(uint32_t v, int at, __half2 z) {
-    const uint32_t x = (v & ((((1u << NB) - 1u) * 0x00010001u) << at)) | 0x64006400u;
-    const float unit = 1.0f / (float)(1 << at);
-    const __half2 c = at == 0 ? __hadd2(*reinterpret_cast<const __half2 *>(&x), __float2half2_rn(-1024.0f))
-                              : __hfma2(*reinterpret_cast<const __half2 *>(&x), __float2half2_rn(unit), __float2half2_rn(-1024.0f * unit));
-    const __half2 y = __hsub2(c, z);
-    return *reinterpret_cast<const uint32_t *>(&y);
+__host__ __device__ constexpr float code_base() { return NB == 8 ? 32768.0f : 128.0f; }
+
+template <int NB>
+__device__ __forceinline__ float code_float(uint32_t bytes, int i) {
+    if constexpr (NB == 8) return __uint_as_float(__byte_perm(bytes, 0x47000000u, 0x7404u + (uint32_t)(i << 4)));
+    else return __uint_as_float(__byte_perm(bytes, 0x43000000u, 0x7044u + (uint32_t)(i << 8)));
 }
 
-// the same 8 codes in the same places, less their zero point
 template <int NB>
-__device__ __forceinline__ uint4 value_chunk8(const uint32_t *w, __half2 z) {
-    if constexpr (NB == 8)
-        return make_uint4(field_less<8>(w[0], 0, z), field_less<8>(w[0] >> 8, 0, z), field_less<8>(w[1], 0, z), field_less<8>(w[1] >> 8, 0, z));
-    else if constexpr (NB == 4)
-        return make_uint4(field_less<4>(w[0], 0, z), field_less<4>(w[0], 4, z), field_less<4>(w[0] >> 8, 0, z), field_less<4>(w[0] >> 8, 4, z));
-    else {
-        const uint32_t v = __byte_perm(w[0], 0, 0x4140);
-        return make_uint4(field_less<2>(v, 0, z), field_less<2>(v, 2, z), field_less<2>(v, 4, z), field_less<2>(v, 6, z));
+__device__ __forceinline__ uint4 value_chunk8(const uint32_t *w, float less, float scale) {
+    uint32_t lo[4], hi[4], y[4];  // the words whose bytes are a pair's codes, and which bytes
+    int il[4], ih[4];
+    if constexpr (NB == 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lo[i] = hi[i] = w[i / 2], il[i] = i & 1, ih[i] = 2 + (i & 1);
+    } else if constexpr (NB == 4) {
+        const uint32_t ev = w[0] & 0x0F0F0F0Fu, od = (w[0] >> 4) & 0x0F0F0F0Fu;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lo[i] = hi[i] = i & 1 ? od : ev, il[i] = i / 2, ih[i] = 2 + i / 2;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lo[i] = hi[i] = (w[0] >> (2 * i)) & 0x03030303u, il[i] = 0, ih[i] = 1;
     }
+    const float2 l2 = make_float2(-less, -less), s2 = make_float2(scale, scale);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = __fmul2_rn(__fadd2_rn(make_float2(code_float<NB>(lo[i], il[i]), code_float<NB>(hi[i], ih[i])), l2), s2);
+        const __half2 h = __floats2half2_rn(v.x, v.y);
+        y[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return make_uint4(y[0], y[1], y[2], y[3]);
 }
 
 __device__ __forceinline__ void sts16(uint32_t at, uint4 v) {
@@ -104,12 +132,6 @@ __device__ __forceinline__ void sts16(uint32_t at, uint4 v) {
 __device__ __forceinline__ float4 lds_f4(uint32_t at) {
     float4 v;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
-    return v;
-}
-
-__device__ __forceinline__ uint2 lds_u2(uint32_t at) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
     return v;
 }
 
@@ -139,14 +161,24 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// mbar_wait, in line: a call would hold registers that the register split does not have
+// mbar_wait, in line (a call would hold registers that the register split does not have) and
+// without naps, which cost a tile's turn some hundred cycles each; a test itself waits a while
 __device__ __forceinline__ bool wait_for(uint32_t addr, uint32_t parity) {
-    for (uint32_t i = 0; i < kMbarWaitLimit; ++i) {
+    for (uint32_t i = 0; i < kMbarWaitLimit; ++i)
         if (mbar_try(addr, parity)) return true;
-        if (i >= 4) __nanosleep(32);
-    }
     return false;
 }
+
+// whether p holds for any of the 64 threads that meet at named barrier `id`
+__device__ __forceinline__ bool any_of_pair(int id, bool p) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 64, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"(id), "r"((uint32_t)p) : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void meet_pair(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
 
 // one lane of a converged warp.  The products' descriptors live in uniform registers: behind this
 // the compiler knows that a single lane issues them, behind `lane == 0` it does not, and moves
@@ -162,6 +194,14 @@ __host__ __device__ constexpr uint32_t tc_idesc(int n, bool along_n) {
     return (1u << 4) | (along_n ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTcRows >> 4) << 24);
 }
 
+// D (+)= A B, both in shared memory
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u) : "memory");
+}
+
 template <int D, int NB, int NG>
 __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const Attn a) {
     using S = TcShape<D, NG>;
@@ -169,7 +209,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile uint32_t failed;  // a wait ran out somewhere
-    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), role = warp >> 2;  // 0 softmax, 1 producers, 2 issue
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), role = warp >> 2;  // 0, 1 softmax, 2 producers, 3 issue
     const int split = blockIdx.x, row0 = (int)blockIdx.y * kTcRows, head = blockIdx.z;
     const uint32_t base = ((uint32_t)__cvta_generic_to_shared(smem_raw) + 1023u) & ~1023u;
     const uint32_t bars = base + S::kBars;
@@ -179,6 +219,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
     const int unit_rows = a.nq * a.share, total_rows = a.batch * unit_rows;
     const int64_t rows = (int64_t)a.batch * a.nq * a.heads;
 
+    // the zero points' step: all but two of its 16 columns stay zero
+    for (int i = tid; i < NG * S::kZqG / 16; i += kTcThreads) sts16(base + S::kZq0 + 16 * i, make_uint4(0, 0, 0, 0));
+    for (int i = tid; i < (2 * NG * S::kZkG + S::kZero) / 16; i += kTcThreads) sts16(base + S::kZk0 + 16 * i, make_uint4(0, 0, 0, 0));
     if (tid == 0) {
         failed = 0;
         for (int s = 0; s < 2; ++s) {
@@ -186,76 +229,105 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
             mbar_init(kv_free + 8 * s, 1);    // the products that read the stage have completed
         }
         mbar_init(s_full, 1);    // scores are complete
-        mbar_init(p_full, 128);  // every softmax thread has stored its weights
+        mbar_init(p_full, kSoftmaxThreads);  // every softmax thread has stored its weights
         mbar_init(done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 8) {
+    if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"((uint32_t)__cvta_generic_to_shared(&tmem_slot)), "n"(S::kCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::);
     }
 
-    // ---- a softmax thread's row: scaled by a power of two that takes its largest magnitude to
-    // [2^14, 2^15), into shared memory in the order of the keys' operands
-    float qs[NG], unit = 0.0f;
+    // ---- a softmax thread's half of a row: scaled by a power of two that takes the row's largest
+    // magnitude to [2^14, 2^15), into shared memory in the order of the keys' operands
+    const int lrow = tid & (kTcRows - 1), hf = (tid >> 7) & 1;
+    float unit = 0.0f;
     int64_t orow = 0, limit = 0;
     bool live = false;
-    if (role == 0) {
-        const int l = row0 + tid;
-        live = l < total_rows;
-        const int lc = live ? l : row0;
-        const int b = lc / unit_rows, i = lc % unit_rows / a.share, h = head * a.share + lc % a.share;
-        orow = ((int64_t)b * a.nq + i) * a.heads + h;
-        int64_t lo;
-        visible<true>(a, own_len(a, b), i, lo, limit);
-        const uint16_t *q = a.q + b * a.q_batch + i * a.q_token + h * a.q_head;
-        uint32_t raw[D / 2];
+    {
+        constexpr int H = D / 2;
+        uint32_t raw[H / 2] = {};
         float big = 0.0f;
-#pragma unroll
-        for (int e = 0; e < D / 2; e += 2) {
-            if (a.q_wide) *reinterpret_cast<uint2 *>(raw + e) = __ldg((const uint2 *)(q + 2 * e));
-            else {
-                raw[e] = __ldg(q + 2 * e) | (uint32_t)__ldg(q + 2 * e + 1) << 16;
-                raw[e + 1] = __ldg(q + 2 * e + 2) | (uint32_t)__ldg(q + 2 * e + 3) << 16;
-            }
-        }
         auto at = [&](int e) {
             const uint32_t w = raw[e / 2];
             return a.bf ? __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16) : to_f32<false>((uint16_t)(e & 1 ? w >> 16 : w));
         };
+        if (role < 2) {
+            const int l = row0 + lrow;
+            live = l < total_rows;
+            const int lc = live ? l : row0;
+            const int b = lc / unit_rows, i = lc % unit_rows / a.share, h = head * a.share + lc % a.share;
+            orow = ((int64_t)b * a.nq + i) * a.heads + h;
+            int64_t lo;
+            visible<true>(a, own_len(a, b), i, lo, limit);
+            const uint16_t *q = a.q + b * a.q_batch + i * a.q_token + h * a.q_head + hf * H;
 #pragma unroll
-        for (int e = 0; e < D; ++e) big = fmaxf(big, fabsf(at(e)));
-        const int ex = big > 0.0f ? min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 100) : 0;
-        const float up = live ? __uint_as_float((uint32_t)(127 + 14 - ex) << 23) : 0.0f;
-        unit = 0x1p24f / __uint_as_float((uint32_t)(127 + 14 - ex) << 23) * a.scale_log2;
+            for (int e = 0; e < H / 2; e += 2) {
+                if (a.q_wide) *reinterpret_cast<uint2 *>(raw + e) = __ldg((const uint2 *)(q + 2 * e));
+                else {
+                    raw[e] = __ldg(q + 2 * e) | (uint32_t)__ldg(q + 2 * e + 1) << 16;
+                    raw[e + 1] = __ldg(q + 2 * e + 2) | (uint32_t)__ldg(q + 2 * e + 3) << 16;
+                }
+            }
 #pragma unroll
-        for (int x = 0; x < NG; ++x) {
-            float sum = 0.0f;
+            for (int e = 0; e < H; ++e) big = fmaxf(big, fabsf(at(e)));
+            sts_f(base + S::kRow0 + (hf * kTcRows + lrow) * 4, big);
+        }
+        __syncthreads();
+        float sum = 0.0f;
+        if (role < 2) {
+            float other;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(base + S::kRow0 + ((hf ^ 1) * kTcRows + lrow) * 4));
+            big = fmaxf(big, other);
+            const int ex = big > 0.0f ? min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 100) : 0;
+            const float up = live ? __uint_as_float((uint32_t)(127 + 14 - ex) << 23) : 0.0f;
+            unit = 0x1p24f / __uint_as_float((uint32_t)(127 + 14 - ex) << 23) * a.scale_log2;
 #pragma unroll
-            for (int o = 0; o < g; o += 8) {  // 8 elements: one stored chunk
+            for (int o8 = 0; o8 < H; o8 += 8) {  // 8 elements: one stored chunk
                 __half y[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float v = at(x * g + o + e) * up;
+                    const float v = at(o8 + e) * up;
                     sum += v;
                     y[place<NB>(e)] = __float2half_rn(v * (1.0f / (float)(1 << place_up<NB>(e))));
                 }
-                const int c = x * (g / 8) + o / (g / 4) * (g / 32) + o % (g / 4) / 8;
-                sts16(base + c / 8 * (kTcRows * 128) + tid * 128 + ((c % 8) ^ (tid & 7)) * 16, *reinterpret_cast<const uint4 *>(y));
+                const int d = hf * H + o8, o = d % g;
+                const int c = d / g * (g / 8) + o / (g / 4) * (g / 32) + o % (g / 4) / 8;
+                sts16(base + c / 8 * (kTcRows * 128) + lrow * 128 + ((c % 8) ^ (lrow & 7)) * 16, *reinterpret_cast<const uint4 *>(y));
             }
-            qs[x] = sum * 0x1p-24f;
+            sum *= 0x1p-24f;
+        }
+        __syncthreads();
+        if (role < 2) sts_f(base + S::kRow0 + (hf * kTcRows + lrow) * 4, sum);
+        __syncthreads();
+        if (role < 2 && hf < NG) {
+            float q_sum = sum;  // two groups: a half each
+            if constexpr (NG == 1) {
+                float other;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(base + S::kRow0 + ((hf ^ 1) * kTcRows + lrow) * 4));
+                q_sum += other;
+            }
+            // its negative, times the 2^6 that the zero points are divided by, in two parts
+            const float v = -64.0f * q_sum;
+            const __half top = __float2half_rn(v), rest = __float2half_rn(v - __half2float(top));
+            const __half2 two = __halves2half2(top, rest);
+            sts_u(base + S::kZq0 + hf * S::kZqG + lrow * 16, *reinterpret_cast<const uint32_t *>(&two));
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        fence_before();
+        __syncthreads();
+        fence_after();
     }
-    fence_before();
-    __syncthreads();
-    fence_after();
     const uint32_t tmem = tmem_slot;
 
     bool ok = true;
-    if (role == 1) {
+    float m = kLowest, vref[NG];
+#pragma unroll
+    for (int x = 0; x < NG; ++x) vref[x] = 0x1p-24f;
+    float2 l2 = make_float2(0.0f, 0.0f);
+    if (role == 2) {
         // ---- producers: thread (t, h) has half h of token t's key and value
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
         constexpr int kVecs = D * NB / 256 + (D * NB % 256 != 0);   // 16-byte pieces of half a row (8 bytes: one)
         constexpr int kHalf = D * NB / 16;                          // bytes of half a row
         const int t = tid & 63, h = (tid >> 6) & 1;
@@ -294,13 +366,39 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
                 x.vm[i] = x.in ? __ldg((const uint32_t *)(a.c.meta[1] + row * NG + i)) : 0u;
             }
         };
+        // 2- and 4-bit codes are fetched a tile ahead; of 8-bit codes two tiles do not fit the registers
+        constexpr bool kAhead = NB < 8;
         Held cur, next;
         load(0, page_of(0), cur);
         int page = page_of(1);
+        float unit_v[NG];  // a power of two, at least the group's every value scale so far
+#pragma unroll
+        for (int x = 0; x < NG; ++x) unit_v[x] = 0x1p-24f;
         for (int i = 0; i < tiles; ++i) {
             const int st = i & 1;
-            load(i + 1, page, next);
-            page = page_of(i + 2);
+            if constexpr (kAhead) {
+                load(i + 1, page, next);
+                page = page_of(i + 2);
+            }
+            float less[NG], scale[NG];
+            // the tile's largest value scale of each group: two warps hold the 64 tokens, twice
+#pragma unroll
+            for (int x = 0; x < NG; ++x) {
+                const float2 vm = __half22float2(*reinterpret_cast<const __half2 *>(&cur.vm[x]));
+                less[x] = vm.y + code_base<NB>();
+                scale[x] = vm.x;
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(vm.x));
+                if (lane == 0) sts_u(base + S::kTops0 + ((warp & 3) * NG + x) * 4, top);
+            }
+            asm volatile("barrier.cta.sync 5, 128;" ::: "memory");
+#pragma unroll
+            for (int x = 0; x < NG; ++x) {
+                uint32_t t0, t1;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(t0) : "r"(base + S::kTops0 + x * 4));
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(t1) : "r"(base + S::kTops0 + (NG + x) * 4));
+                unit_v[x] = fmaxf(unit_v[x], __uint_as_float((max(t0, t1) + 0x007fffffu) & 0x7f800000u));
+                scale[x] *= 1.0f / unit_v[x];
+            }
             if (i >= 2 && ok) ok = wait_for(kv_free + 8 * st, (uint32_t)((i >> 1) - 1) & 1u);
             const uint32_t kt = base + S::kStage0 + st * 2 * S::kTile, vt = kt + S::kTile, mt = base + S::kMeta0 + st * S::kMeta;
 #pragma unroll
@@ -319,70 +417,76 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
                 const int cx = h * (CH / 2) + x;
                 const int kr = x % (D / 32), kg = kr / (g / 32), kc = kg * (g / 8) + cx / (D / 32) * (g / 32) + kr % (g / 32);
                 const int vr = x % (D / 64), vg = vr / (g / 64), vc = vg * (g / 8) + cx / (D / 64) * (g / 64) + vr % (g / 64);
-                const uint32_t z = __byte_perm(cur.vm[vg], 0, 0x3232);
                 sts16(kt + kc / 8 * (kTcTokens * 128) + t * 128 + ((kc % 8) ^ (t & 7)) * 16, key_chunk8<NB>(kw));
                 sts16(vt + vc / 8 * (kTcTokens * 128) + t * 128 + ((vc % 8) ^ (t & 7)) * 16,
-                      value_chunk8<NB>(vw, *reinterpret_cast<const __half2 *>(&z)));
+                      value_chunk8<NB>(vw, less[vg], scale[vg]));
             }
-            uint32_t top = 0;
+            if (h == 0) {
 #pragma unroll
-            for (int x = 0; x < NG; ++x) {
-                const float2 km = __half22float2(*reinterpret_cast<const __half2 *>(&cur.km[x]));
-                const float vs = __low2float(*reinterpret_cast<const __half2 *>(&cur.vm[x]));
-                if (h == 0) {
+                for (int x = 0; x < NG; ++x) {
+                    const float2 km = __half22float2(*reinterpret_cast<const __half2 *>(&cur.km[x]));
+                    const __half2 z = __float2half2_rn(km.y * 0x1p-6f);
                     sts_f(mt + (x * kTcTokens + t) * 4, km.x);
-                    sts_f(mt + ((NG + x) * kTcTokens + t) * 4, -km.y);
-                } else {
-                    sts_f(mt + ((2 * NG + x) * kTcTokens + t) * 4, vs);
-                    top = max(top, __float_as_uint(vs));
+                    sts_u(base + S::kZk0 + (st * NG + x) * S::kZkG + t * 16, *reinterpret_cast<const uint32_t *>(&z));
                 }
+                const uint32_t in = __ballot_sync(0xffffffffu, cur.in);
+                if (lane == 0) sts_u(mt + NG * kTcTokens * 4 + (t >> 5) * 4, in);
+            } else if (t == 0) {
+#pragma unroll
+                for (int x = 0; x < NG; ++x) sts_f(mt + NG * kTcTokens * 4 + 8 + x * 4, unit_v[x]);
             }
-            const uint32_t in = __ballot_sync(0xffffffffu, cur.in), most = __reduce_max_sync(0xffffffffu, top);
-            if (lane == 0) sts_u(mt + 3 * NG * kTcTokens * 4 + (h == 0 ? 0 : 8) + (t >> 5) * 4, h == 0 ? in : most);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             mbar_arrive(kv_full + 8 * st);
-            cur = next;
+            if constexpr (kAhead) {
+                cur = next;
+            } else {
+                load(i + 1, page, cur);
+                page = page_of(i + 2);
+            }
         }
         if (!ok) failed = 1;
-    } else if (role == 2) {
+    } else if (role == 3) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-        if (warp == 8 && elected()) {
-            constexpr uint32_t s_idesc = tc_idesc(kTcTokens, false), o_idesc = tc_idesc(g, true);
+        if (warp == 12 && elected()) {
+            constexpr uint32_t s_idesc = tc_idesc(kTcTokens, false), o_idesc = tc_idesc(D, true);
+            if (ok) ok = wait_for(kv_full, 0u);
             for (int i = 0; i < tiles; ++i) {
                 const int st = i & 1;
                 const uint32_t kt = base + S::kStage0 + st * 2 * S::kTile, vt = kt + S::kTile;
-                if (ok) ok = wait_for(kv_full + 8 * st, (uint32_t)(i >> 1) & 1u);
                 fence_after();
                 if (ok) {
 #pragma unroll
-                    for (int x = 0; x < NG; ++x)
+                    for (int x = 0; x < NG; ++x) {
+                        // the zero points: pieces of 8 rows of 16 bytes without a swizzle, 128 bytes apart; the
+                        // second 8 of 16 columns are the zeros
+                        const uint32_t zq = S::kZq0 + x * S::kZqG, zk = S::kZk0 + (st * NG + x) * S::kZkG;
+                        mma_ss(tmem + x * kTcTokens, umma_desc(base + zq, S::kZero0 - zq, 128, 0),
+                               umma_desc(base + zk, S::kZero0 - zk, 128, 0), s_idesc, false);
 #pragma unroll
                         for (int k = 0; k < g / 16; ++k) {
                             const int e = x * g + k * 16;  // 16 elements: 32 bytes along a swizzled row
-                            const uint64_t da = umma_desc(base + e / 64 * (kTcRows * 128) + e % 64 * 2, 16, 1024, 2);
-                            const uint64_t db = umma_desc(kt + e / 64 * (kTcTokens * 128) + e % 64 * 2, 16, 1024, 2);
-                            asm volatile(
-                                "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                                "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                                ::"r"(tmem + x * kTcTokens), "l"(da), "l"(db), "r"(s_idesc), "r"(k > 0 ? 1u : 0u) : "memory");
+                            mma_ss(tmem + x * kTcTokens, umma_desc(base + e / 64 * (kTcRows * 128) + e % 64 * 2, 16, 1024, 2),
+                                   umma_desc(kt + e / 64 * (kTcTokens * 128) + e % 64 * 2, 16, 1024, 2), s_idesc, true);
                         }
+                    }
                 }
                 umma_commit(s_full);
+                // the next tile, so that its scores follow this one's values at once
+                if (ok && i + 1 < tiles) ok = wait_for(kv_full + 8 * (st ^ 1), (uint32_t)((i + 1) >> 1) & 1u);
                 if (ok) ok = wait_for(p_full, (uint32_t)i & 1u);
                 fence_after();
                 if (ok) {
 #pragma unroll
-                    for (int x = 0; x < NG; ++x)
-#pragma unroll
-                        for (int k = 0; k < kTcTokens / 16; ++k) {
-                            // 16 tokens: two groups of 8 rows; blocks of 64 elements lie a tile's rows apart
-                            const uint64_t db = umma_desc(vt + x * g / 64 * (kTcTokens * 128) + k * 2048, kTcTokens * 128, 1024, 2);
-                            asm volatile(
-                                "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                                "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                                ::"r"(tmem + S::kOCol + x * g), "r"(tmem + x * (kTcTokens / 2) + 8 * k), "l"(db), "r"(o_idesc),
-                                  "r"(i > 0 || k > 0 ? 1u : 0u) : "memory");
-                        }
+                    for (int k = 0; k < kTcTokens / 16; ++k) {
+                        // 16 tokens: two groups of 8 rows; blocks of 64 elements lie a tile's rows apart.
+                        // A half's weights lie over its own scores of group 0
+                        const uint64_t db = umma_desc(vt + k * 2048, kTcTokens * 128, 1024, 2);
+                        asm volatile(
+                            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                            ::"r"(tmem + S::kOCol), "r"(tmem + k / 2 * 32 + k % 2 * 8), "l"(db), "r"(o_idesc),
+                              "r"(i > 0 || k > 0 ? 1u : 0u) : "memory");
+                    }
                 }
                 umma_commit(kv_free + 8 * st);
             }
@@ -392,35 +496,35 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
-        float m = kLowest, bound = -INFINITY, vref = 0x1p-24f, vin = kWeightUnit * 0x1p24f;
-        float2 l2 = make_float2(0.0f, 0.0f);
+        constexpr int N = kTcTokens / 2;  // tokens of a thread
+        constexpr float kUp = 6.0f;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16), mine = lanes + 32 * hf;
+        const int pair = 1 + (warp & 3);  // the named barrier of the two warps that share rows
+        const uint32_t row_at = base + S::kRow0 + lrow * 4;
+        float bound = -INFINITY;
         const int span = (int)(to - from);
         const int lim = live ? (int)min(max(limit - from, (int64_t)0), (int64_t)span) : span;  // a row that is not there sees all
         const int all = __reduce_min_sync(0xffffffffu, lim);
         for (int i = 0; i < tiles; ++i) {
-            const int st = i & 1, t0 = i * kTcTokens;
+            const int st = i & 1, t0 = i * kTcTokens + N * hf;
             const uint32_t mt = base + S::kMeta0 + st * S::kMeta;
             if (ok) ok = wait_for(kv_full + 8 * st, (uint32_t)(i >> 1) & 1u);
             if (ok) ok = wait_for(s_full, (uint32_t)i & 1u);
             fence_after();
-            float2 s[kTcTokens / 2];
+            float2 s[N / 2];
 #pragma unroll
-            for (int c = 0; c < kTcTokens / 16; ++c) {
+            for (int c = 0; c < N / 16; ++c) {
                 float x[NG][16];
 #pragma unroll
-                for (int y = 0; y < NG; ++y) tmem_ld16(lanes + y * kTcTokens + 16 * c, x[y]);
+                for (int y = 0; y < NG; ++y) tmem_ld16(mine + y * kTcTokens + 16 * c, x[y]);
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                     float2 r[2];
 #pragma unroll
                     for (int y = 0; y < NG; ++y) {
-                        const float4 ks = lds_f4(mt + (y * kTcTokens + 16 * c + e) * 4);
-                        const float4 kz = lds_f4(mt + ((NG + y) * kTcTokens + 16 * c + e) * 4);
-                        const float2 q2 = make_float2(qs[y], qs[y]);
-                        const float2 a0 = __ffma2_rn(make_float2(kz.x, kz.y), q2, make_float2(x[y][e], x[y][e + 1]));
-                        const float2 a1 = __ffma2_rn(make_float2(kz.z, kz.w), q2, make_float2(x[y][e + 2], x[y][e + 3]));
+                        const float4 ks = lds_f4(mt + (y * kTcTokens + N * hf + 16 * c + e) * 4);
+                        const float2 a0 = make_float2(x[y][e], x[y][e + 1]), a1 = make_float2(x[y][e + 2], x[y][e + 3]);
                         r[0] = y == 0 ? __fmul2_rn(make_float2(ks.x, ks.y), a0) : __ffma2_rn(make_float2(ks.x, ks.y), a0, r[0]);
                         r[1] = y == 0 ? __fmul2_rn(make_float2(ks.z, ks.w), a1) : __ffma2_rn(make_float2(ks.z, ks.w), a1, r[1]);
                     }
@@ -428,87 +532,94 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
                     s[8 * c + e / 2 + 1] = r[1];
                 }
             }
-            const uint2 valid = lds_u2(mt + 3 * NG * kTcTokens * 4), most = lds_u2(mt + 3 * NG * kTcTokens * 4 + 8);
-            if (t0 + kTcTokens > all || (valid.x & valid.y) != 0xffffffffu) {
+            const float4 said = lds_f4(mt + NG * kTcTokens * 4);  // valid[2], the values' units
+            const uint32_t valid = __float_as_uint(hf ? said.y : said.x);
+            const float to_v[2] = {said.z, said.w};
+            if (t0 + N > all || valid != 0xffffffffu) {
 #pragma unroll
-                for (int e = 0; e < kTcTokens; ++e) {
-                    const bool seen = ((e < 32 ? valid.x : valid.y) >> (e & 31) & 1u) && t0 + e < lim;
+                for (int e = 0; e < N; ++e) {
+                    const bool seen = (valid >> e & 1u) && t0 + e < lim;
                     float &v = e & 1 ? s[e / 2].y : s[e / 2].x;
                     v = seen ? v : -INFINITY;
                 }
             }
-            float top = fmaxf(s[0].x, s[0].y);
+            float tops[4];
 #pragma unroll
-            for (int e = 1; e < kTcTokens / 2; ++e) top = fmaxf(top, fmaxf(s[e].x, s[e].y));
-            const float vs = __uint_as_float(max(most.x, most.y));
-            if (__any_sync(0xffffffffu, top > bound || vs > vref)) {
-                const float up = fmaxf(vref, __uint_as_float((__float_as_uint(vs) + 0x007fffffu) & 0x7f800000u));
-                top = fmaxf(top * unit, m);
+            for (int e = 0; e < 4; ++e) tops[e] = fmaxf(s[e].x, s[e].y);
+#pragma unroll
+            for (int e = 4; e < N / 2; ++e) tops[e & 3] = fmaxf(tops[e & 3], fmaxf(s[e].x, s[e].y));
+            float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+            bool more = top > bound;
+#pragma unroll
+            for (int x = 0; x < NG; ++x) more |= to_v[x] > vref[x];
+            if (any_of_pair(pair, more)) {
+                sts_f(row_at + hf * kTcRows * 4, top);
+                meet_pair(pair);
+                float other;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(row_at + (hf ^ 1) * kTcRows * 4));
+                top = fmaxf(fmaxf(top, other) * unit, m);
                 const float f = exp2_fast(m - top);
-                const float fo = f * (vref / up);
-                vref = up;
-                vin = kWeightUnit / up;
+                float fo[NG];
+#pragma unroll
+                for (int x = 0; x < NG; ++x) {
+                    fo[x] = f * (vref[x] / to_v[x]);
+                    vref[x] = to_v[x];
+                }
                 m = top;
                 bound = top == kLowest ? -INFINITY : (top + kLag) / unit;
                 l2.x *= f;
                 l2.y *= f;
                 if (i > 0) {  // the products up to tile i - 1 have completed: S of tile i came after them
 #pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {
+                    for (int c = 0; c < D / 32; ++c) {
                         float x[16];
-                        tmem_ld16(lanes + S::kOCol + 16 * c, x);
+                        tmem_ld16(lanes + S::kOCol + hf * (D / 2) + 16 * c, x);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) x[e] *= fo;
-                        tmem_st16(lanes + S::kOCol + 16 * c, reinterpret_cast<const uint32_t *>(x));
+                        for (int e = 0; e < 16; ++e) x[e] *= fo[NG == 1 ? 0 : hf];  // a half of two groups is one
+                        tmem_st16(lanes + S::kOCol + hf * (D / 2) + 16 * c, reinterpret_cast<const uint32_t *>(x));
                     }
                 }
             }
-            const float2 u2 = make_float2(unit, unit), m2 = make_float2(-m, -m), v2 = make_float2(vin, vin);
+            // weights: p times 2^6, to keep small ones normal in fp16
+            const float2 u2 = make_float2(unit, unit), m2 = make_float2(kUp - m, kUp - m);
+            uint32_t w[N / 2];
 #pragma unroll
-            for (int e = 0; e < kTcTokens / 2; ++e) {
+            for (int e = 0; e < N / 2; ++e) {
                 const float2 y = __ffma2_rn(s[e], u2, m2);
-                s[e] = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-                l2 = __fadd2_rn(l2, s[e]);
-                s[e] = __fmul2_rn(s[e], v2);
+                const float2 p = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+                l2 = __fadd2_rn(l2, p);
+                const __half2 h = __floats2half2_rn(p.x, p.y);
+                w[e] = *reinterpret_cast<const uint32_t *>(&h);
             }
-#pragma unroll
-            for (int y = 0; y < NG; ++y)
-#pragma unroll
-                for (int c = 0; c < kTcTokens / 32; ++c) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const float4 v = lds_f4(mt + ((2 * NG + y) * kTcTokens + 32 * c + 2 * e) * 4);
-                        const float2 w0 = __fmul2_rn(s[16 * c + e], make_float2(v.x, v.y));
-                        const float2 w1 = __fmul2_rn(s[16 * c + e + 1], make_float2(v.z, v.w));
-                        const __half2 h0 = __floats2half2_rn(w0.x, w0.y), h1 = __floats2half2_rn(w1.x, w1.y);
-                        w[e] = *reinterpret_cast<const uint32_t *>(&h0);
-                        w[e + 1] = *reinterpret_cast<const uint32_t *>(&h1);
-                    }
-                    tmem_st16(lanes + y * (kTcTokens / 2) + 16 * c, w);
-                }
+            tmem_st16(mine, w);
             tmem_wait_st();
             fence_before();
             mbar_arrive(p_full);
         }
-        // ---- the chunk's result, normalised by itself
+        // ---- the chunk's result, normalised by itself: half of the elements each
         if (ok) ok = wait_for(done, 0u);
-        ok = __all_sync(0xffffffffu, ok && !failed);
+        ok = ok && !failed;
         fence_after();
-        const float sum = l2.x + l2.y;
-        const float f = !ok ? __int_as_float(0x7fc00000) : sum > 0.0f ? vref / kWeightUnit / sum : 0.0f;
+        meet_pair(pair);  // the other's maximum has been read
+        sts_f(row_at + hf * kTcRows * 4, ok ? l2.x + l2.y : -1.0f);
+        meet_pair(pair);
+        float other;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(row_at + (hf ^ 1) * kTcRows * 4));
+        ok = ok && other >= 0.0f;
+        const float sum = l2.x + l2.y + other;
+        const float f = !ok ? __int_as_float(0x7fc00000) : sum > 0.0f ? vref[NG == 1 ? 0 : hf] / sum : 0.0f;
         float *out = a.part_o + (split * rows + orow) * D;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
+        for (int c = 0; c < D / 32; ++c) {
             float x[16];
-            tmem_ld16(lanes + S::kOCol + 16 * c, x);
+            tmem_ld16(lanes + S::kOCol + hf * (D / 2) + 16 * c, x);
             tmem_wait_ld();
             if (live) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    // operand chunk 2c + k: of group x8, run p, 8 elements from d on
-                    const int x8 = 2 * c + k, grp = x8 / (g / 8), in_g = x8 % (g / 8);
+                    // operand chunk x8: of a group, run p, 8 elements from d on
+                    const int x8 = hf * (D / 16) + 2 * c + k, grp = x8 / (g / 8), in_g = x8 % (g / 8);
                     const int d = grp * g + in_g / (g / 64) * (g / 8) + in_g % (g / 64) * 8;
                     float y[8];
 #pragma unroll
@@ -518,15 +629,17 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
                 }
             }
         }
-        if (live) a.part_lse[split * rows + orow] = !ok ? f : sum > 0.0f ? m + log2f(sum) : -INFINITY;
+        if (live && hf == 0) a.part_lse[split * rows + orow] = !ok ? f : sum > 0.0f ? m - kUp + log2f(sum) : -INFINITY;
     }
     fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 12) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kCols));
     }
 }
+
+static_assert(2 * (TcShape<128, 2>::kSmem + 1024) <= 228 * 1024, "two CTAs on an SM");
 
 template <int D, int NB, int NG>
 cudaError_t launch(const Attn &a, int row_tiles, cudaStream_t st) {
