@@ -741,12 +741,15 @@ __global__ void __launch_bounds__(kAttnThreads, (Shape<D, NB, NG, RB>::kCtas)) h
         }
     }
     if (a.ctas > 0 && threadIdx.x == 0) a.cuts[blockIdx.x] = cut;
+    // the join waits for this kernel only, and may read what the prefix's wrote: that one first
+    if (a.prefix_splits > 0) wait_prerequisite();
 }
 
 // The prefix: CTA (x, y, z) has chunk x for block y of the batch's rows and key head z.
 template <int D, int NB, int NG, int RB>
 __global__ void __launch_bounds__(kAttnThreads, (Shape<D, NB, NG, RB>::kCtas)) hqq_kv_prefix_kernel(const Attn a) {
     extern __shared__ __align__(16) unsigned char smem[];
+    allow_dependents();  // the sequences' own tokens need nothing of this
     const int64_t rows = (int64_t)a.batch * a.nq * a.heads;
     const uint32_t units = (uint32_t)(a.prefix_chunk / kUnit);
     attend_segment<D, NB, NG, RB, true>(a, 0, (int)blockIdx.y * 8 * RB, (int)blockIdx.z, blockIdx.x * units,
@@ -892,14 +895,24 @@ int make_attn_plan(const hqq_kv_cache_t *cache, int64_t batch, int64_t nq, int64
     return HQQ_OK;
 }
 
-template <typename K>
-cudaError_t launch_attn(K kernel, dim3 grid, int smem, const Attn &a, cudaStream_t st) {
+// `beside`: may start before the kernel in front of it has ended
+template <typename K, typename... Args>
+cudaError_t launch_attn(K kernel, dim3 grid, int threads, int smem, bool beside, cudaStream_t st, Args... args) {
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    kernel<<<grid, kAttnThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = beside ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 int run_attention(const hqq_kv_cache_t *cache, const Attn &a, const AttnPlan &pl, cudaStream_t st) {
@@ -914,29 +927,21 @@ int run_attention(const hqq_kv_cache_t *cache, const Attn &a, const AttnPlan &pl
             if (pl.prefix_tc)
                 e = launch_prefix_tc(*cache, a, pl.prefix_row_blocks, st);
             else if (rows_per_cta(D, (int64_t)a.nq * a.share * a.batch) == 16)
-                e = launch_attn(hqq_kv_prefix_kernel<D, NB, NG, kWide>, grid, Shape<D, NB, NG, kWide>::kSmem, a, st);
+                e = launch_attn(hqq_kv_prefix_kernel<D, NB, NG, kWide>, grid, kAttnThreads, Shape<D, NB, NG, kWide>::kSmem, false, st, a);
             else
-                e = launch_attn(hqq_kv_prefix_kernel<D, NB, NG, 1>, grid, Shape<D, NB, NG, 1>::kSmem, a, st);
+                e = launch_attn(hqq_kv_prefix_kernel<D, NB, NG, 1>, grid, kAttnThreads, Shape<D, NB, NG, 1>::kSmem, false, st, a);
             if (e != cudaSuccess) return HQQ_ERR_CUDA;
         }
         const dim3 grid(a.ctas ? a.ctas : (unsigned)pairs);
+        const bool beside = pl.prefix_splits > 0;
         if (pl.pair_rows == 16)
-            e = launch_attn(hqq_kv_attn_kernel<D, NB, NG, kWide>, grid, Shape<D, NB, NG, kWide>::kSmem, a, st);
+            e = launch_attn(hqq_kv_attn_kernel<D, NB, NG, kWide>, grid, kAttnThreads, Shape<D, NB, NG, kWide>::kSmem, beside, st, a);
         else
-            e = launch_attn(hqq_kv_attn_kernel<D, NB, NG, 1>, grid, Shape<D, NB, NG, 1>::kSmem, a, st);
+            e = launch_attn(hqq_kv_attn_kernel<D, NB, NG, 1>, grid, kAttnThreads, Shape<D, NB, NG, 1>::kSmem, beside, st, a);
         if (e != cudaSuccess) return HQQ_ERR_CUDA;
-        if (a.ctas || pl.prefix_splits) {
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-            attr[0].val.programmaticStreamSerializationAllowed = 1;
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(pl.prefix_splits ? (unsigned)pairs : (unsigned)a.ctas, std::min(pl.pair_rows, a.nq * a.share));
-            cfg.blockDim = dim3(32 * kJoinWarps);
-            cfg.stream = st;
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
-            e = cudaLaunchKernelEx(&cfg, hqq_kv_join_kernel<D>, a, pl.pair_rows);
-        }
+        if (a.ctas || pl.prefix_splits)
+            e = launch_attn(hqq_kv_join_kernel<D>, dim3(pl.prefix_splits ? (unsigned)pairs : (unsigned)a.ctas, std::min(pl.pair_rows, a.nq * a.share)),
+                            32 * kJoinWarps, 0, true, st, a, pl.pair_rows);
         return e == cudaSuccess ? HQQ_OK : HQQ_ERR_CUDA;
     });
 }

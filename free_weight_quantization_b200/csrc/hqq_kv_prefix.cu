@@ -41,9 +41,9 @@ using namespace hqq_kv;
 
 constexpr int kTcThreads = 512, kSoftmaxThreads = 256;
 // registers of a thread: 64 at launch (two CTAs of 512), divided so that the sum is the same
-constexpr int kTcLaunchRegs = 64, kSoftmaxRegs = 80, kProducerRegs = 72, kIssueRegs = 24;
+constexpr int kTcLaunchRegs = 64, kSoftmaxRegs = 80, kProducerRegs = 64, kIssueRegs = 32;
 static_assert(2 * kSoftmaxRegs + kProducerRegs + kIssueRegs <= 4 * kTcLaunchRegs, "setmaxnreg draws on the launch's registers");
-static_assert(kSoftmaxRegs >= kTcLaunchRegs && kProducerRegs >= kTcLaunchRegs && kIssueRegs <= kTcLaunchRegs,
+static_assert(kSoftmaxRegs > kTcLaunchRegs && kProducerRegs == kTcLaunchRegs && kIssueRegs < kTcLaunchRegs,
               "an increase to fewer registers, or a decrease to more, is an illegal instruction");
 
 template <int D, int NG>
@@ -194,12 +194,26 @@ __host__ __device__ constexpr uint32_t tc_idesc(int n, bool along_n) {
     return (1u << 4) | (along_n ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTcRows >> 4) << 24);
 }
 
+// A descriptor's low word has the address and the leading offset, the high word the rest; in 16-byte
+// units the address carries nowhere, so that a step along an operand is one 32-bit addition.
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo, uint32_t layout) { return (sbo >> 4) | 1u << 14 | layout << 29; }
+
+__device__ __forceinline__ uint32_t desc_lo(uint32_t at, uint32_t lbo) { return (at >> 4) | (lbo >> 4) << 16; }
+
 // D (+)= A B, both in shared memory
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u) : "memory");
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}"
+        ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(add ? 1u : 0u) : "memory");
+}
+
+// the same with A in tensor memory
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}"
+        ::"r"(d), "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(add ? 1u : 0u) : "memory");
 }
 
 template <int D, int NB, int NG>
@@ -207,6 +221,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
     using S = TcShape<D, NG>;
     constexpr int g = D / NG, CH = D / 8;  // 8-code chunks of a row
     extern __shared__ unsigned char smem_raw[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the sequences' own tokens need nothing of this
     __shared__ uint32_t tmem_slot;
     __shared__ volatile uint32_t failed;  // a wait ran out somewhere
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), role = warp >> 2;  // 0, 1 softmax, 2 producers, 3 issue
@@ -238,86 +253,79 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::);
     }
 
-    // ---- a softmax thread's half of a row: scaled by a power of two that takes the row's largest
+    __syncthreads();  // the zeros are in place
+    // ---- the rows, 8 elements to a thread: each row scaled by a power of two that takes its largest
     // magnitude to [2^14, 2^15), into shared memory in the order of the keys' operands
-    const int lrow = tid & (kTcRows - 1), hf = (tid >> 7) & 1;
+    {
+        constexpr int T = D / 8;  // threads of a row: neighbours in a warp
+        for (int at = tid; at < kTcRows * T; at += kTcThreads) {  // whole warps: 128 T is a multiple of 32
+            const int rr = at / T, d = at % T * 8, l = row0 + rr;
+            const bool there = l < total_rows;
+            const int lc = there ? l : row0;
+            const int b = lc / unit_rows, i = lc % unit_rows / a.share, h = head * a.share + lc % a.share;
+            const uint16_t *q = a.q + b * a.q_batch + i * a.q_token + h * a.q_head + d;
+            uint32_t raw[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (a.q_wide) {
+                    *reinterpret_cast<uint2 *>(raw + 2 * e) = __ldg((const uint2 *)(q + 4 * e));
+                } else {
+                    raw[2 * e] = __ldg(q + 4 * e) | (uint32_t)__ldg(q + 4 * e + 1) << 16;
+                    raw[2 * e + 1] = __ldg(q + 4 * e + 2) | (uint32_t)__ldg(q + 4 * e + 3) << 16;
+                }
+            }
+            float v[8], big = 0.0f, sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t w = there ? raw[e / 2] : 0u;
+                v[e] = a.bf ? __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16) : to_f32<false>((uint16_t)(e & 1 ? w >> 16 : w));
+                big = fmaxf(big, fabsf(v[e]));
+            }
+#pragma unroll
+            for (int x = 1; x < T; x *= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
+            const int ex = big > 0.0f ? min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 100) : 0;
+            const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+            __half y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[e] *= up;
+                sum += v[e];
+                y[place<NB>(e)] = __float2half_rn(v[e] * (1.0f / (float)(1 << place_up<NB>(e))));
+            }
+            const int o = d % g, c = d / g * (g / 8) + o / (g / 4) * (g / 32) + o % (g / 4) / 8;
+            sts16(base + c / 8 * (kTcRows * 128) + rr * 128 + ((c % 8) ^ (rr & 7)) * 16, *reinterpret_cast<const uint4 *>(y));
+#pragma unroll
+            for (int x = 1; x < g / 8; x *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+            if (d % g == 0) {
+                // the zero points' step: the negative sum, times the 2^6 that they are divided by, in two parts
+                const float z = -64.0f * 0x1p-24f * sum;
+                const __half top = __float2half_rn(z), rest = __float2half_rn(z - __half2float(top));
+                const __half2 two = __halves2half2(top, rest);
+                sts_u(base + S::kZq0 + d / g * S::kZqG + rr * 16, *reinterpret_cast<const uint32_t *>(&two));
+            }
+            if (d == 0) sts_f(base + S::kMeta0 + rr * 4, 0x1p24f / up * a.scale_log2);  // until the tiles come
+        }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+    // a softmax thread's row
     float unit = 0.0f;
     int64_t orow = 0, limit = 0;
     bool live = false;
-    {
-        constexpr int H = D / 2;
-        uint32_t raw[H / 2] = {};
-        float big = 0.0f;
-        auto at = [&](int e) {
-            const uint32_t w = raw[e / 2];
-            return a.bf ? __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16) : to_f32<false>((uint16_t)(e & 1 ? w >> 16 : w));
-        };
-        if (role < 2) {
-            const int l = row0 + lrow;
-            live = l < total_rows;
-            const int lc = live ? l : row0;
-            const int b = lc / unit_rows, i = lc % unit_rows / a.share, h = head * a.share + lc % a.share;
-            orow = ((int64_t)b * a.nq + i) * a.heads + h;
-            int64_t lo;
-            visible<true>(a, own_len(a, b), i, lo, limit);
-            const uint16_t *q = a.q + b * a.q_batch + i * a.q_token + h * a.q_head + hf * H;
-#pragma unroll
-            for (int e = 0; e < H / 2; e += 2) {
-                if (a.q_wide) *reinterpret_cast<uint2 *>(raw + e) = __ldg((const uint2 *)(q + 2 * e));
-                else {
-                    raw[e] = __ldg(q + 2 * e) | (uint32_t)__ldg(q + 2 * e + 1) << 16;
-                    raw[e + 1] = __ldg(q + 2 * e + 2) | (uint32_t)__ldg(q + 2 * e + 3) << 16;
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < H; ++e) big = fmaxf(big, fabsf(at(e)));
-            sts_f(base + S::kRow0 + (hf * kTcRows + lrow) * 4, big);
-        }
-        __syncthreads();
-        float sum = 0.0f;
-        if (role < 2) {
-            float other;
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(base + S::kRow0 + ((hf ^ 1) * kTcRows + lrow) * 4));
-            big = fmaxf(big, other);
-            const int ex = big > 0.0f ? min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 100) : 0;
-            const float up = live ? __uint_as_float((uint32_t)(127 + 14 - ex) << 23) : 0.0f;
-            unit = 0x1p24f / __uint_as_float((uint32_t)(127 + 14 - ex) << 23) * a.scale_log2;
-#pragma unroll
-            for (int o8 = 0; o8 < H; o8 += 8) {  // 8 elements: one stored chunk
-                __half y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float v = at(o8 + e) * up;
-                    sum += v;
-                    y[place<NB>(e)] = __float2half_rn(v * (1.0f / (float)(1 << place_up<NB>(e))));
-                }
-                const int d = hf * H + o8, o = d % g;
-                const int c = d / g * (g / 8) + o / (g / 4) * (g / 32) + o % (g / 4) / 8;
-                sts16(base + c / 8 * (kTcRows * 128) + lrow * 128 + ((c % 8) ^ (lrow & 7)) * 16, *reinterpret_cast<const uint4 *>(y));
-            }
-            sum *= 0x1p-24f;
-        }
-        __syncthreads();
-        if (role < 2) sts_f(base + S::kRow0 + (hf * kTcRows + lrow) * 4, sum);
-        __syncthreads();
-        if (role < 2 && hf < NG) {
-            float q_sum = sum;  // two groups: a half each
-            if constexpr (NG == 1) {
-                float other;
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(base + S::kRow0 + ((hf ^ 1) * kTcRows + lrow) * 4));
-                q_sum += other;
-            }
-            // its negative, times the 2^6 that the zero points are divided by, in two parts
-            const float v = -64.0f * q_sum;
-            const __half top = __float2half_rn(v), rest = __float2half_rn(v - __half2float(top));
-            const __half2 two = __halves2half2(top, rest);
-            sts_u(base + S::kZq0 + hf * S::kZqG + lrow * 16, *reinterpret_cast<const uint32_t *>(&two));
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        fence_before();
-        __syncthreads();
-        fence_after();
+    const int lrow = tid & (kTcRows - 1), hf = (tid >> 7) & 1;  // two threads to a row, 32 tokens of a tile each
+    if (role < 2) {
+        const int l = row0 + lrow;
+        live = l < total_rows;
+        const int lc = live ? l : row0;
+        const int b = lc / unit_rows, i = lc % unit_rows / a.share, h = head * a.share + lc % a.share;
+        orow = ((int64_t)b * a.nq + i) * a.heads + h;
+        int64_t lo;
+        visible<true>(a, own_len(a, b), i, lo, limit);
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(unit) : "r"(base + S::kMeta0 + lrow * 4));
     }
+    fence_before();
+    __syncthreads();
+    fence_after();
     const uint32_t tmem = tmem_slot;
 
     bool ok = true;
@@ -327,7 +335,6 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
     float2 l2 = make_float2(0.0f, 0.0f);
     if (role == 2) {
         // ---- producers: thread (t, h) has half h of token t's key and value
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
         constexpr int kVecs = D * NB / 256 + (D * NB % 256 != 0);   // 16-byte pieces of half a row (8 bytes: one)
         constexpr int kHalf = D * NB / 16;                          // bytes of half a row
         const int t = tid & 63, h = (tid >> 6) & 1;
@@ -449,46 +456,53 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
         if (warp == 12 && elected()) {
             constexpr uint32_t s_idesc = tc_idesc(kTcTokens, false), o_idesc = tc_idesc(D, true);
-            if (ok) ok = wait_for(kv_full, 0u);
-            for (int i = 0; i < tiles; ++i) {
-                const int st = i & 1;
-                const uint32_t kt = base + S::kStage0 + st * 2 * S::kTile, vt = kt + S::kTile;
-                fence_after();
-                if (ok) {
+            constexpr uint32_t hi = desc_hi(1024, 2), z_hi = desc_hi(128, 0);
+            const uint32_t tm = tmem;
+            const uint32_t q_lo = desc_lo(base, 16), k_lo = desc_lo(base + S::kStage0, 16);
+            // 16 tokens of values: two groups of 8 rows; blocks of 64 elements lie a tile's rows apart
+            const uint32_t v_lo = desc_lo(base + S::kStage0 + S::kTile, kTcTokens * 128);
+            // the zero points: pieces of 8 rows of 16 bytes without a swizzle, 128 bytes apart; the second 8
+            // of 16 columns are the zeros behind them
+            const uint32_t z0 = base >> 4;
+            auto scores = [&](auto stage) {
+                constexpr int st = decltype(stage)::value;
 #pragma unroll
-                    for (int x = 0; x < NG; ++x) {
-                        // the zero points: pieces of 8 rows of 16 bytes without a swizzle, 128 bytes apart; the
-                        // second 8 of 16 columns are the zeros
-                        const uint32_t zq = S::kZq0 + x * S::kZqG, zk = S::kZk0 + (st * NG + x) * S::kZkG;
-                        mma_ss(tmem + x * kTcTokens, umma_desc(base + zq, S::kZero0 - zq, 128, 0),
-                               umma_desc(base + zk, S::kZero0 - zk, 128, 0), s_idesc, false);
+                for (int x = 0; x < NG; ++x) {
+                    constexpr uint32_t q0 = S::kZq0, k0 = S::kZk0 + st * NG * S::kZkG;
+                    const uint32_t zq = q0 + x * S::kZqG, zk = k0 + x * S::kZkG;
+                    mma_ss(tm + x * kTcTokens, z0 + (zq / 16 | (S::kZero0 - zq) / 16 << 16), z0 + (zk / 16 | (S::kZero0 - zk) / 16 << 16),
+                           z_hi, s_idesc, false);
 #pragma unroll
-                        for (int k = 0; k < g / 16; ++k) {
-                            const int e = x * g + k * 16;  // 16 elements: 32 bytes along a swizzled row
-                            mma_ss(tmem + x * kTcTokens, umma_desc(base + e / 64 * (kTcRows * 128) + e % 64 * 2, 16, 1024, 2),
-                                   umma_desc(kt + e / 64 * (kTcTokens * 128) + e % 64 * 2, 16, 1024, 2), s_idesc, true);
-                        }
+                    for (int k = 0; k < g / 16; ++k) {
+                        const int e = x * g + k * 16;  // 16 elements: 32 bytes along a swizzled row
+                        mma_ss(tm + x * kTcTokens, q_lo + (e / 64 * (kTcRows * 128) + e % 64 * 2) / 16,
+                               k_lo + (st * 2 * S::kTile + e / 64 * (kTcTokens * 128) + e % 64 * 2) / 16, hi, s_idesc, true);
                     }
                 }
+            };
+            auto outputs = [&](auto stage, bool add) {
+                constexpr int st = decltype(stage)::value;
+                // a half's weights lie over its own scores of group 0
+#pragma unroll
+                for (int k = 0; k < kTcTokens / 16; ++k)
+                    mma_ts(tm + S::kOCol, tm + k / 2 * 32 + k % 2 * 8, v_lo + (st * 2 * S::kTile + k * 2048) / 16, hi, o_idesc, add || k > 0);
+            };
+            auto tile = [&](int i, auto stage) {
+                constexpr int st = decltype(stage)::value;
+                fence_after();
+                if (ok) scores(stage);
                 umma_commit(s_full);
                 // the next tile, so that its scores follow this one's values at once
                 if (ok && i + 1 < tiles) ok = wait_for(kv_full + 8 * (st ^ 1), (uint32_t)((i + 1) >> 1) & 1u);
                 if (ok) ok = wait_for(p_full, (uint32_t)i & 1u);
                 fence_after();
-                if (ok) {
-#pragma unroll
-                    for (int k = 0; k < kTcTokens / 16; ++k) {
-                        // 16 tokens: two groups of 8 rows; blocks of 64 elements lie a tile's rows apart.
-                        // A half's weights lie over its own scores of group 0
-                        const uint64_t db = umma_desc(vt + k * 2048, kTcTokens * 128, 1024, 2);
-                        asm volatile(
-                            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                            ::"r"(tmem + S::kOCol), "r"(tmem + k / 2 * 32 + k % 2 * 8), "l"(db), "r"(o_idesc),
-                              "r"(i > 0 || k > 0 ? 1u : 0u) : "memory");
-                    }
-                }
+                if (ok) outputs(stage, i > 0);
                 umma_commit(kv_free + 8 * st);
+            };
+            if (ok) ok = wait_for(kv_full, 0u);
+            for (int i = 0; i < tiles; i += 2) {
+                tile(i, std::integral_constant<int, 0>{});
+                if (i + 1 < tiles) tile(i + 1, std::integral_constant<int, 1>{});
             }
             if (!ok) failed = 1;
             umma_commit(done);
@@ -609,25 +623,33 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
         ok = ok && other >= 0.0f;
         const float sum = l2.x + l2.y + other;
         const float f = !ok ? __int_as_float(0x7fc00000) : sum > 0.0f ? vref[NG == 1 ? 0 : hf] / sum : 0.0f;
-        float *out = a.part_o + (split * rows + orow) * D;
+        // by way of shared memory (everything there has been read), so that a row goes out in one piece:
+        // rows 16 bytes more than D floats apart, which meet in no bank
+        constexpr uint32_t kRow = D * 4 + 16;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
             float x[16];
             tmem_ld16(lanes + S::kOCol + hf * (D / 2) + 16 * c, x);
             tmem_wait_ld();
-            if (live) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    // operand chunk x8: of a group, run p, 8 elements from d on
-                    const int x8 = hf * (D / 16) + 2 * c + k, grp = x8 / (g / 8), in_g = x8 % (g / 8);
-                    const int d = grp * g + in_g / (g / 64) * (g / 8) + in_g % (g / 64) * 8;
-                    float y[8];
+            for (int k = 0; k < 2; ++k) {
+                // operand chunk x8: of a group, run p, 8 elements from d on
+                const int x8 = hf * (D / 16) + 2 * c + k, grp = x8 / (g / 8), in_g = x8 % (g / 8);
+                const int d = grp * g + in_g / (g / 64) * (g / 8) + in_g % (g / 64) * 8;
+                uint32_t y[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = sum > 0.0f || !ok ? x[8 * k + place<NB>(e)] * f : 0.0f;
-                    *reinterpret_cast<float4 *>(out + d) = make_float4(y[0], y[1], y[2], y[3]);
-                    *reinterpret_cast<float4 *>(out + d + 4) = make_float4(y[4], y[5], y[6], y[7]);
-                }
+                for (int e = 0; e < 8; ++e) y[e] = sum > 0.0f || !ok ? __float_as_uint(x[8 * k + place<NB>(e)] * f) : 0u;
+                sts16(base + (uint32_t)lrow * kRow + d * 4, make_uint4(y[0], y[1], y[2], y[3]));
+                sts16(base + (uint32_t)lrow * kRow + d * 4 + 16, make_uint4(y[4], y[5], y[6], y[7]));
             }
+        }
+        meet_pair(pair);
+        for (int r = 16 * hf; r < 16 * hf + 16; ++r) {  // half of the pair's 32 rows each
+            const int64_t to_row = __shfl_sync(0xffffffffu, orow, r);
+            const int rr = 32 * (warp & 3) + r;
+            if (row0 + rr >= total_rows) break;
+            if (lane < D / 4)
+                *reinterpret_cast<float4 *>(a.part_o + (split * rows + to_row) * D + 4 * lane) = lds_f4(base + (uint32_t)rr * kRow + 16 * lane);
         }
         if (live && hf == 0) a.part_lse[split * rows + orow] = !ok ? f : sum > 0.0f ? m - kUp + log2f(sum) : -INFINITY;
     }
@@ -639,6 +661,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
     }
 }
 
+static_assert(TcShape<128, 1>::kBars >= kTcRows * (128 * 4 + 16) && TcShape<64, 1>::kBars >= kTcRows * (64 * 4 + 16),
+              "room for the results");
 static_assert(2 * (TcShape<128, 2>::kSmem + 1024) <= 228 * 1024, "two CTAs on an SM");
 
 template <int D, int NB, int NG>
