@@ -113,45 +113,107 @@ __device__ __forceinline__ uint64_t take_codes(const uint8_t *row, int d) {
     }
 }
 
+// 8 codes as four pairs (e, e + 4) of 16-bit whole numbers, the order in which a word of codes falls
+// apart into halves
+struct Codes8 {
+    uint32_t pair[4];
+};
+
+template <int NB>
+__device__ __forceinline__ uint64_t join_codes(const Codes8 &c) {
+    if constexpr (NB == 8) {
+        const uint32_t a = c.pair[0] | c.pair[1] << 8, b = c.pair[2] | c.pair[3] << 8;
+        return (uint64_t)__byte_perm(a, b, 0x7632) << 32 | __byte_perm(a, b, 0x5410);
+    } else {
+        const uint32_t w = c.pair[0] | c.pair[1] << NB | c.pair[2] << (2 * NB) | c.pair[3] << (3 * NB);
+        return NB == 4 ? w : __byte_perm(w, 0, 0x4420);
+    }
+}
+
+template <int NB>
+__device__ __forceinline__ Codes8 split_codes(uint64_t codes) {
+    Codes8 c;
+    if constexpr (NB == 8) {
+        const uint32_t lo = (uint32_t)codes, hi = (uint32_t)(codes >> 32);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c.pair[i] = __byte_perm(lo, hi, 0x0400u + 0x0101u * i) & 0x00FF00FFu;
+    } else {
+        const uint32_t w = NB == 4 ? (uint32_t)codes : __byte_perm((uint32_t)codes, 0, 0x4140);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c.pair[i] = (w >> (NB * i)) & (((1u << NB) - 1u) * 0x00010001u);
+    }
+    return c;
+}
+
 // (code - zero) * scale of 8 codes, rounded once more to 16 bits
-template <int NB, bool BF>
-__device__ __forceinline__ uint4 values_of(uint64_t codes, float scale, float zero) {
+template <bool BF>
+__device__ __forceinline__ uint4 values_of(const Codes8 &c, float scale, float zero) {
+    float2 v[4];  // elements i and i + 4
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // 2^23 + c and back: c, exactly
+        const float2 q = make_float2(__uint_as_float(__byte_perm(c.pair[i], 0x4B000000u, 0x7610)),
+                                     __uint_as_float(__byte_perm(c.pair[i], 0x4B000000u, 0x7632)));
+        v[i] = __fmul2_rn(__fadd2_rn(__fadd2_rn(q, make_float2(-8388608.0f, -8388608.0f)), make_float2(-zero, -zero)),
+                          make_float2(scale, scale));
+    }
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        uint32_t h[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t c = (uint32_t)(codes >> (NB * (2 * i + j))) & ((1u << NB) - 1u);
-            const float q = __uint_as_float(0x4B000000u | c) - 8388608.0f;  // c, exactly
-            h[j] = from_f32<BF>(__fmul_rn(__fsub_rn(q, zero), scale));
+        const float a = i < 2 ? v[2 * i].x : v[2 * i - 4].y, b = i < 2 ? v[2 * i + 1].x : v[2 * i - 3].y;
+        if constexpr (BF) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        } else {
+            const __half2 h = __floats2half2_rn(a, b);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        w[i] = h[0] | h[1] << 16;
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// max(a, b) of pairs of 16-bit values; a NaN stays
+template <bool BF>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (BF) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Quantises 8 values of one row; the D/NG/8 threads of its group are neighbours in a warp.
 template <int D, int NB, int NG, int P, bool BF>
-__device__ __forceinline__ void append_part(const StoreArgs &a, int side, int64_t token, int head, int d,
+__device__ __forceinline__ void append_part(const StoreArgs &a, int side, uint32_t r, int d,
                                             int64_t row, bool inside, bool live, const uint4 raw) {
     constexpr int g = D / NG;
     constexpr float top = (float)((1 << NB) - 1);
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    // the largest value and the largest negated one, in 16 bits: exact, and half the work
+    uint32_t most = max2<BF>(max2<BF>(w[0], w[1]), max2<BF>(w[2], w[3]));
+    uint32_t less = max2<BF>(max2<BF>(w[0] ^ 0x80008000u, w[1] ^ 0x80008000u), max2<BF>(w[2] ^ 0x80008000u, w[3] ^ 0x80008000u));
+    uint32_t ends = max2<BF>(__byte_perm(most, less, 0x5410), __byte_perm(most, less, 0x7632));  // (largest, -least)
+#pragma unroll
+    for (int m = 1; m < g / 8; m *= 2) ends = max2<BF>(ends, __shfl_xor_sync(0xffffffffu, ends, m));
+    float hi = to_f32<BF>((uint16_t)ends), lo = -to_f32<BF>((uint16_t)(ends >> 16));
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        x[i] = fminf(fmaxf(to_f32<BF>((uint16_t)(w[i / 2] >> (16 * (i & 1)))), -65504.0f), 65504.0f);
-    float lo = x[0], hi = x[0];
+        x[i] = BF ? __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16) : to_f32<BF>((uint16_t)(w[i / 2] >> (16 * (i & 1))));
+    // a NaN, an infinity or a value that fp16 has not: clamped, all threads of the warp in step
+    if (__any_sync(0xffffffffu, !(hi <= 65504.0f && lo >= -65504.0f))) {
+        hi = -65504.0f;
+        lo = 65504.0f;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-    }
+        for (int i = 0; i < 8; ++i) {
+            x[i] = fminf(fmaxf(x[i], -65504.0f), 65504.0f);
+            lo = fminf(lo, x[i]);
+            hi = fmaxf(hi, x[i]);
+        }
 #pragma unroll
-    for (int m = 1; m < g / 8; m *= 2) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
+        for (int m = 1; m < g / 8; m *= 2) {
+            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
+            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
+        }
     }
     const float step = __fdiv_rn(__fsub_rn(hi, lo), top);
     const float least = __fmul_rn(fmaxf(fabsf(lo), fabsf(hi)), 0x1p-10f);
@@ -159,32 +221,37 @@ __device__ __forceinline__ void append_part(const StoreArgs &a, int side, int64_
     const float scale = __half2float(scale_h), inv = __frcp_rn(scale);
     const __half zero_h = __float2half_rn(__fmul_rn(-lo, inv));
     const float zero = __half2float(zero_h);
-    uint64_t codes = 0;
+    Codes8 c;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float t = fminf(fmaxf(__fadd_rn(__fmul_rn(x[i], inv), zero), 0.0f), top);
-        const uint32_t c = __float_as_uint(t + 8388608.0f) & 0xFFu;  // rint, ties to even
-        codes |= (uint64_t)c << (NB * i);
+    for (int i = 0; i < 4; ++i) {
+        // one by one: the packed product and sum were seen merged into one operation with one rounding
+        const float2 t = make_float2(__fadd_rn(__fmul_rn(x[i], inv), zero), __fadd_rn(__fmul_rn(x[i + 4], inv), zero));
+        // rint, ties to even, into the low bits; the scale and zero point are rounded, so that it can
+        // lie a little outside 0 .. 2^b - 1
+        const float2 u = __fadd2_rn(t, make_float2(12582912.0f, 12582912.0f));
+        const uint32_t p = __byte_perm(__float_as_uint(u.x), __float_as_uint(u.y), 0x5410);
+        c.pair[i] = __vmins2(__vmaxs2(p, 0u), (uint32_t)((1 << NB) - 1) * 0x00010001u);
     }
     if (live) {
-        put_codes<D, NB, NG, P>(a.c.codes[side] + row * (D * NB / 8), d, codes);
+        put_codes<D, NB, NG, P>(a.c.codes[side] + row * (D * NB / 8), d, join_codes<NB>(c));
         if (d % g == 0) a.c.meta[side][row * NG + d / g] = __halves2half2(scale_h, zero_h);
     }
     if (inside && a.y[side]) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (live) v = values_of<NB, BF>(codes, scale, zero);
-        *(uint4 *)(a.y[side] + (token * a.c.heads + head) * D + d) = v;
+        if (live) v = values_of<BF>(c, scale, zero);
+        *(uint4 *)(a.y[side] + (int64_t)r * D + d) = v;
     }
 }
 
-template <bool BF>
-__device__ __forceinline__ uint4 load8(const uint16_t *p, bool wide) {
-    if (wide) return __ldg((const uint4 *)p);
+// 8 values that need not be aligned: a call, or its 8 loads go along as predicated-off ones
+__device__ __noinline__ uint4 load8_singly(const uint16_t *p) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = (uint32_t)__ldg(p + 2 * i) | (uint32_t)__ldg(p + 2 * i + 1) << 16;
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
+
+__device__ __forceinline__ uint4 load8(const uint16_t *p, bool wide) { return wide ? __ldg((const uint4 *)p) : load8_singly(p); }
 
 // One thread for 8 values of a key and the same 8 of its value: D / 8 threads a row.  Bound by the
 // bytes it moves: every load and store of a warp covers whole 32-byte sectors, and two 16-byte
@@ -192,29 +259,29 @@ __device__ __forceinline__ uint4 load8(const uint16_t *p, bool wide) {
 template <int D, int NB, int NG, bool BF>
 __global__ void __launch_bounds__(kStoreThreads) hqq_kv_append_kernel(const StoreArgs a) {
     constexpr int kRows = kStoreThreads / (D / kPerThread);
-    const int64_t rows = a.tokens * a.c.heads;
-    const int64_t r0 = (int64_t)blockIdx.x * kRows + threadIdx.x / (D / kPerThread);
-    const int64_t r = r0 < rows ? r0 : rows - 1;  // whole warps take part in the exchanges below
+    const uint32_t rows = (uint32_t)a.tokens * a.c.heads;  // below 2^31
+    const uint32_t r0 = blockIdx.x * kRows + threadIdx.x / (D / kPerThread);
+    const uint32_t r = min(r0, rows - 1);  // whole warps take part in the exchanges below
     const int d = (int)(threadIdx.x % (D / kPerThread)) * kPerThread;
-    const int64_t token = r / a.c.heads;
+    const uint32_t token = r / (uint32_t)a.c.heads;
     const int head = (int)(r - token * a.c.heads);
-    const uint4 k = load8<BF>(a.x[0] + token * a.token_stride[0] + head * a.head_stride[0] + d, a.wide);
-    const uint4 v = load8<BF>(a.x[1] + token * a.token_stride[1] + head * a.head_stride[1] + d, a.wide);
+    const uint4 k = load8(a.x[0] + token * a.token_stride[0] + head * a.head_stride[0] + d, a.wide);
+    const uint4 v = load8(a.x[1] + token * a.token_stride[1] + head * a.head_stride[1] + d, a.wide);
     const int64_t slot = __ldg(a.slots + token);
     const int64_t page = slot >> a.c.page_shift;
     const bool inside = r0 < rows, live = inside && slot >= 0 && page < a.c.pages;
     const int64_t row = live ? row_of(a.c, page, head, (int)(slot & ((1 << a.c.page_shift) - 1))) : 0;
-    append_part<D, NB, NG, kKeyPieces, BF>(a, 0, token, head, d, row, inside, live, k);
-    append_part<D, NB, NG, kValuePieces, BF>(a, 1, token, head, d, row, inside, live, v);
+    append_part<D, NB, NG, kKeyPieces, BF>(a, 0, r, d, row, inside, live, k);
+    append_part<D, NB, NG, kValuePieces, BF>(a, 1, r, d, row, inside, live, v);
 }
 
 template <int D, int NB, int NG, bool BF>
 __global__ void __launch_bounds__(kStoreThreads) hqq_kv_read_kernel(const StoreArgs a) {
     constexpr int kRows = kStoreThreads / (D / kPerThread), g = D / NG;
-    const int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / (D / kPerThread);
-    if (r >= a.tokens * a.c.heads) return;
+    const uint32_t r = blockIdx.x * kRows + threadIdx.x / (D / kPerThread);
+    if (r >= (uint32_t)a.tokens * a.c.heads) return;
     const int d = (int)(threadIdx.x % (D / kPerThread)) * kPerThread;
-    const int64_t token = r / a.c.heads;
+    const uint32_t token = r / (uint32_t)a.c.heads;
     const int head = (int)(r - token * a.c.heads);
     const int64_t slot = __ldg(a.slots + token);
     const int64_t page = slot >> a.c.page_shift;
@@ -225,11 +292,11 @@ __global__ void __launch_bounds__(kStoreThreads) hqq_kv_read_kernel(const StoreA
         const uint64_t vc = take_codes<D, NB, NG, kValuePieces>(a.c.codes[1] + row * (D * NB / 8), d);
         const float2 km = __half22float2(__ldg(a.c.meta[0] + row * NG + d / g));
         const float2 vm = __half22float2(__ldg(a.c.meta[1] + row * NG + d / g));
-        k = values_of<NB, BF>(kc, km.x, km.y);
-        v = values_of<NB, BF>(vc, vm.x, vm.y);
+        k = values_of<BF>(split_codes<NB>(kc), km.x, km.y);
+        v = values_of<BF>(split_codes<NB>(vc), vm.x, vm.y);
     }
-    if (a.y[0]) *(uint4 *)(a.y[0] + r * D + d) = k;
-    if (a.y[1]) *(uint4 *)(a.y[1] + r * D + d) = v;
+    if (a.y[0]) *(uint4 *)(a.y[0] + (int64_t)r * D + d) = k;
+    if (a.y[1]) *(uint4 *)(a.y[1] + (int64_t)r * D + d) = v;
 }
 
 template <bool APPEND>
