@@ -860,6 +860,7 @@ int make_attn_plan(const hqq_kv_cache_t *cache, int64_t batch, int64_t nq, int64
         batch * nq > INT32_MAX / heads)
         return HQQ_ERR_UNSUPPORTED;
     *pl = AttnPlan{};
+    if (batch * nq == 0) return HQQ_OK;  // no rows: nothing is launched
     const int64_t rows = nq * (heads / c.heads);
     const int ru = pl->pair_rows = rows_per_cta(cache->head_dim, rows);
     pl->row_blocks = (int)ceil_div(rows, ru);

@@ -311,8 +311,8 @@ class KVCache:
                                       ("v_meta", v_meta, meta, torch.float16)):
             if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
                 raise HqqError(f"KVCache: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
-            if not t.is_cuda or t.device != k_codes.device:
-                raise HqqError("KVCache: the tensors must live on one CUDA device")
+        if any(not t.is_cuda or t.device != k_codes.device for t in (k_codes, v_codes, k_meta, v_meta)):
+            raise HqqError("KVCache: the tensors must live on one CUDA device")
         self.k_codes, self.v_codes, self.k_meta, self.v_meta = k_codes, v_codes, k_meta, v_meta
         self.num_pages, self.kv_heads, self.page_size = pages, heads, page_size
         self.head_dim, self.nbits, self.group_size = head_dim, nbits, group_size

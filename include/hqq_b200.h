@@ -300,7 +300,7 @@ size_t hqq_kv_attention_workspace_bytes(const hqq_kv_cache_t *cache, int64_t bat
  *   workspace >= hqq_kv_attention_workspace_bytes(..) bytes, 16-byte aligned; contents on entry do
  *             not matter; must not be used by anything else until this call's work has finished
  * Results do not depend on what else runs: sums are joined in a fixed order.
- * Limits: batch * kv_heads <= 65535, nq <= 65535, max_len < 2^31.
+ * Limits: batch, nq <= 65535, max_len < 2^31, heads * batch * nq < 2^31.
  */
 int hqq_kv_attention(const hqq_kv_cache_t *cache, const void *q, int dtype, int64_t batch, int64_t nq,
                      int64_t heads, int64_t q_batch_stride, int64_t q_token_stride,
