@@ -16,17 +16,20 @@
 //
 // Sixteen warps, two CTAs on an SM:
 //   * four producer warps turn the codes of a tile into operands in shared memory (128-byte
-//     swizzle; keys K-major, values with the elements along the rows), two stages, and the
-//     metadata into binary32 arrays;
-//   * one lane issues the tcgen05.mma: S_g (128 x 64, binary32, tensor memory), then O_g with the
+//     swizzle; keys K-major, values with the elements along the rows), two stages;
+//   * one lane issues the tcgen05.mma: S_g (128 x 64, binary32, tensor memory), then O with the
 //     weights as the A operand in tensor memory, where they take the place of S;
 //   * eight softmax warps: two threads have a row, 32 tokens of a tile each; they read their
 //     scores from tensor memory, keep a common running maximum and a sum each, and write the
 //     weights.  O is rescaled in tensor memory only when the maximum has grown by more than 2^8, or
-//     a larger value scale appears.  (With one thread a row, four warps, the turn of a tile took
-//     5500 cycles, 3300 of them here: a warp alone on its scheduler waits for itself.)
+//     a larger value scale appears.  (Four warps with a thread to a row: 114 us where this takes 104.)
 // The two CTAs of an SM cover each other's turns: while one's scores are in its softmax warps the
 // other's products run.
+//
+// What bounds it: the turn of a tile, scores - weights - products, which tensor memory leaves no room
+// to overlap within a CTA (S of two groups and O fill its 256 columns).  64 sequences x 32 heads
+// behind 32768 tokens, 8 key heads, 4 bits, g = 64: 85 us, half of the issue slots, 400 TFLOP/s; the
+// products alone would take 21.  8-bit codes, which the producers cannot fetch a tile ahead: 98.
 //
 // Waits on mbarriers are bounded: one that runs out (none should) makes the CTA write NaN; the other
 // roles' waits run out in their turn, and the CTA ends.

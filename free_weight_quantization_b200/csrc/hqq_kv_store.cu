@@ -253,9 +253,10 @@ __device__ __noinline__ uint4 load8_singly(const uint16_t *p) {
 
 __device__ __forceinline__ uint4 load8(const uint16_t *p, bool wide) { return wide ? __ldg((const uint4 *)p) : load8_singly(p); }
 
-// One thread for 8 values of a key and the same 8 of its value: D / 8 threads a row.  Bound by the
-// bytes it moves: every load and store of a warp covers whole 32-byte sectors, and two 16-byte
-// loads are in flight for each thread.
+// One thread for 8 values of a key and the same 8 of its value: D / 8 threads a row, every load and
+// store of a warp covers whole 32-byte sectors, two 16-byte loads are in flight for each thread.
+// 8192 tokens x 32 heads x 128, with the values returned: 67 us where its bytes take 47; 440
+// instructions a warp keep the issue slots 80 % busy.
 template <int D, int NB, int NG, bool BF>
 __global__ void __launch_bounds__(kStoreThreads) hqq_kv_append_kernel(const StoreArgs a) {
     constexpr int kRows = kStoreThreads / (D / kPerThread);
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kStoreThreads) hqq_kv_append_kernel(const Stor
 
 // The same threads with kReadRows rows each, a block's rows apart: a slot's number, then its codes
 // and metadata, are two trips to memory, on which several rows go together (one row a thread: 41 us
-// for 32768 tokens x 8 heads, bound by the wait).
+// for 32768 tokens x 8 heads x 128, bound by the wait; four 34, its bytes take 26).
 constexpr int kReadRows = 4;
 
 template <int D, int NB, int NG, bool BF>
