@@ -822,19 +822,37 @@ __global__ void __launch_bounds__(32 * kJoinWarps) hqq_kv_join_kernel(const Attn
     }
 #pragma unroll
     for (int x = 16; x > 0; x /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    // four parts at a time, all their loads on the way before the first is used
+    constexpr int kAtOnce = 4, kVec = E < 4 ? E : 4;
     float acc[E], sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < E; ++i) acc[i] = 0.0f;
-#pragma unroll 4
-    for (int p = warp; p < parts; p += kJoinWarps) {
-        find(p, o, e);
-        const float f = exp2_fast(__ldcg(e) - top);  // a part that saw nothing holds zeros
-        sum += f;
+    for (int p = warp; p < parts; p += kJoinWarps * kAtOnce) {
+        float x[kAtOnce][E], at[kAtOnce];
 #pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] = __fmaf_rn(__ldcg(o + lane + 32 * i), f, acc[i]);
+        for (int u = 0; u < kAtOnce; ++u) {
+            at[u] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < E; ++i) x[u][i] = 0.0f;
+            if (p + u * kJoinWarps >= parts) continue;
+            find(p + u * kJoinWarps, o, e);
+            at[u] = __ldcg(e);
+#pragma unroll
+            for (int i = 0; i < E; i += kVec) {
+                if constexpr (kVec == 4) *reinterpret_cast<float4 *>(x[u] + i) = __ldcg((const float4 *)(o + lane * E + i));
+                else *reinterpret_cast<float2 *>(x[u] + i) = __ldcg((const float2 *)(o + lane * E + i));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const float f = exp2_fast(at[u] - top);  // a part that saw nothing holds zeros
+            sum += f;
+#pragma unroll
+            for (int i = 0; i < E; ++i) acc[i] = __fmaf_rn(x[u][i], f, acc[i]);
+        }
     }
 #pragma unroll
-    for (int i = 0; i < E; ++i) acc_s[warp][lane + 32 * i] = acc[i];
+    for (int i = 0; i < E; ++i) acc_s[warp][lane * E + i] = acc[i];
     if (lane == 0) sum_s[warp] = sum;
     __syncthreads();
     for (int d = threadIdx.x; d < D; d += 32 * kJoinWarps) {
@@ -850,9 +868,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) hqq_kv_join_kernel(const Attn
     }
 }
 
-// rows of a key head over the whole batch above which the prefix goes to the tcgen05 kernel, which
-// takes 128 at a time: 4096 tokens x 8 key heads, 32 rows 20 us here, 64 rows 31 here and 25 there
-constexpr int kTcMinRows = 32;
+// Rows of a key head over the whole batch above which the prefix goes to the tcgen05 kernel, which
+// takes 128 at a time.  In us, 8 key heads, that kernel / the one above: 4096 tokens 32 rows 25 / 21,
+// 64 rows 25 / 22, 128 rows 27 / 30; 32768 tokens 32 rows 57 / 39, 64 rows 58 / 59.
+constexpr int kTcMinRows = 64;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

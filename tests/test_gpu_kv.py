@@ -11,7 +11,7 @@ tolerance counts the roundings of the kernel, u = 2^-11 being half a step of fp1
     and the sums over n tokens add is below (n + 16) 2^-23 relative, taken on sum_t p_t |v_td|, with
     the codes and zero points summed apart: |v_td| is replaced by scale_tg (c_td + |zero_tg|);
   * the output is rounded to its type: half a step relative to itself;
-  * behind a prefix with more than 32 rows on a key head, the values too are rounded to fp16 once, after a
+  * behind a prefix with more than 64 rows on a key head, the values too are rounded to fp16 once, after a
     zero point that is off by at most 2^-17 of a step (2^-9 of one of 255): another u * |v_td| and that
     share of scale_tg.
 """
@@ -157,7 +157,7 @@ def context(cache, table, count):
 def attend(cache, q, tables, lens, window=0, prefix=(None, 0), scale=None, hidden=None):
     """out, lse and the error bound of out before its rounding, all in 64 bits.  hidden[b]: tokens of
     sequence b that are not seen whatever their place."""
-    rounded = prefix[1] > 0 and q.shape[0] * q.shape[1] * q.shape[2] // cache.kv_heads > 32
+    rounded = prefix[1] > 0 and q.shape[0] * q.shape[1] * q.shape[2] // cache.kv_heads > 64
     step = 2.0 ** -9 if cache.nbits == 8 else 2.0 ** -17
     B, nq, H, D = q.shape
     share = H // cache.kv_heads
