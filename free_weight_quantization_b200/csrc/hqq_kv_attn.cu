@@ -156,8 +156,6 @@ __device__ __forceinline__ const T *pinned(const T *p) {
     return (const T *)((uint64_t)pinned((uint32_t)(v >> 32)) << 32 | pinned((uint32_t)v));
 }
 
-// Rows of one key head are numbered l = (b - b0) * nq * share + i * share + (h - head * share).
-
 // What a kernel of this layout keeps in shared memory and how many of its CTAs an SM holds.
 template <int D, int NB, int NG, int RB>
 struct Shape {
@@ -243,8 +241,9 @@ __device__ __forceinline__ Start find_start(const Attn &a, Start *shared) {
     return begin < total ? *shared : Start{total, begin, total, a.batch};
 }
 
-// One segment: the blocks of tokens [first unit, last unit) of a pair, by all warps of the CTA.
-// `to_part`: where a result goes that is not the pair's whole; see the end.
+// One segment: units [unit0, unit1) of a pair's tokens, by all warps of the CTA.  The result goes to
+// part_o and part_lse, by the row of the pair (by_slot) or of the output, or to the outputs themselves
+// where there are none.
 template <int D, int NB, int NG, int RB, bool PREFIX>
 __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, int head, uint32_t unit0, uint32_t unit1,
                                                float *part_o, float *part_lse, bool by_slot, unsigned char *smem) {
@@ -259,7 +258,8 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
     const int unit_rows = a.nq * a.share;                       // rows of one sequence and key head
     const int total_rows = PREFIX ? a.batch * unit_rows : unit_rows;
 
-    // output row of local row l
+    // rows of one key head are numbered l = (b - b0) * nq * share + i * share + (h - head * share);
+    // the output's row of that
     auto out_row = [&](int l) -> int64_t {
         const int b = b0 + l / unit_rows, i = l % unit_rows / a.share, h = l % a.share;
         return ((int64_t)b * a.nq + i) * a.heads + head * a.share + h;
@@ -282,19 +282,19 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
 
     // ---- this thread's share of the query rows: on its way while the page table is
     constexpr int T = kAttnThreads / RU, E = D / T;  // threads of a row, elements of a thread
-            const int rr = threadIdx.x / T, d0 = threadIdx.x % T * E, lrow = row0 + rr;
-            const bool live = lrow < total_rows;
-            const int lc = live ? lrow : row0;
-            const int b = b0 + lc / unit_rows, i = lc % unit_rows / a.share, h = head * a.share + lc % a.share;
-            const uint16_t *q = a.q + b * a.q_batch + i * a.q_token + h * a.q_head + d0;
-            uint32_t raw[E / 2];
-            if (a.q_wide) {
+    const int rr = threadIdx.x / T, d0 = threadIdx.x % T * E, lrow = row0 + rr;
+    const bool live = lrow < total_rows;
+    const int lc = live ? lrow : row0;
+    const int b = b0 + lc / unit_rows, i = lc % unit_rows / a.share, h = head * a.share + lc % a.share;
+    const uint16_t *q = a.q + b * a.q_batch + i * a.q_token + h * a.q_head + d0;
+    uint32_t raw[E / 2];
+    if (a.q_wide) {
 #pragma unroll
-                for (int e = 0; e < E / 4; ++e) *reinterpret_cast<uint2 *>(raw + 2 * e) = __ldg((const uint2 *)q + e);
-            } else {
+        for (int e = 0; e < E / 4; ++e) *reinterpret_cast<uint2 *>(raw + 2 * e) = __ldg((const uint2 *)q + e);
+    } else {
 #pragma unroll
-                for (int e = 0; e < E / 2; ++e) raw[e] = __ldg(q + 2 * e) | (uint32_t)__ldg(q + 2 * e + 1) << 16;
-            }
+        for (int e = 0; e < E / 2; ++e) raw[e] = __ldg(q + 2 * e) | (uint32_t)__ldg(q + 2 * e + 1) << 16;
+    }
 
     // ---- copies: this warp's block number `it` of the segment into stage it % kStages
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * (S::kStages * S::kStage);

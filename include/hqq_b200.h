@@ -314,7 +314,9 @@ int hqq_kv_attention(const hqq_kv_cache_t *cache, const void *q, int dtype, int6
  * tokens of prefix_pages followed by its own lens[b] tokens of pages[b], and the prefix is read
  * once for the whole batch.  prefix_pages: [ceil(prefix_len / page_size)] device int32; the last
  * page may be partly filled (a sequence's own tokens begin on a page of their own).  The queries
- * are the last nq tokens of prefix and own tokens together.
+ * are the last nq tokens of prefix and own tokens together.  With more than 64 query rows (batch *
+ * nq * heads / kv_heads) on a key head and group_size >= 64, head_dim <= 128 the prefix runs on the
+ * tcgen05 tensor cores; p_t and the values (code - zero) * scale are then rounded to fp16, once each.
  */
 int hqq_kv_prefix_attention(const hqq_kv_cache_t *cache, const void *q, int dtype, int64_t batch,
                             int64_t nq, int64_t heads, int64_t q_batch_stride,

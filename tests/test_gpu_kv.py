@@ -105,6 +105,7 @@ def test_append_and_read_bit_exact(hqq, D, nb, g, dtype):
     v[4] = 100.0 + 0.01 * torch.arange(D)
     k[5, 0, :5] = torch.tensor([math.inf, -math.inf, 60000.0, -60000.0, 0.0])
     v[6] = 2.0 ** -24 * torch.arange(D)
+    v[10, 1, 3], k[11, 2, D - 1] = math.nan, math.nan
     slots = rng.permutation(6 * ps)[:n]
     slots[7], slots[8], slots[9] = -1, 6 * ps, -(2 ** 40)   # padding, and past the pool
     s = torch.from_numpy(slots).cuda()
