@@ -36,7 +36,7 @@
 // What bounds it: per block of 16 tokens a warp has some 310 instructions at 4 bits and D = 128, 104
 // of them to take the codes apart, and the integer units issue every other cycle.  Between 8192 and
 // 16384 tokens of 64 sequences x 8 key heads a token more costs 1.19 of what its bytes cost at the
-// card's copy rate (6.55 TB/s); a call of 64 x 4096 takes 78 us (46 for its bytes), of which some 20
+// card's copy rate (6.55 TB/s); a call of 64 x 4096 takes 77 us (46 for its bytes), of which some 20
 // are the way in (lengths, page table, first codes: three trips to memory), the change from one pair
 // to the next, and the join.  2-bit codes take the same instructions for half the bytes (74 us, 26
 // for the bytes); 16 rows a CTA 119 us for twice the products.
@@ -898,9 +898,11 @@ int make_attn_plan(const hqq_kv_cache_t *cache, int64_t batch, int64_t nq, int64
     int64_t span = max_len;
     if (window > 0) span = std::min<int64_t>(span, window + nq + kBlock);
     const int64_t units = kFixed + std::max<int64_t>(1, ceil_div(span, kUnit)), pairs = batch * c.heads * pl->row_blocks;
-    // Pairs of at most 512 tokens have a CTA each, and no join: one launch, and no more steps in a
+    // Pairs of at most 1024 tokens have a CTA each, and no join: one launch, and no more steps in a
     // row than the join costs.  Longer ones are shared among all SMs; a share is at least 4 units.
-    if (units > kFixed + 8)
+    // In us, a CTA each / shared (32 heads on 8): 1 x 1000 tokens 12 / 12, 16 x 1000 14 / 18,
+    // 64 x 1000 26 / 34; 1 x 2000 20 / 12, 16 x 2000 20 / 21.
+    if (units > kFixed + 16)
         pl->ctas = (int)std::min<int64_t>(kSms * per_sm, std::max<int64_t>(pairs, ceil_div(pairs * units, 4)));
     if (pairs > INT32_MAX / units) return HQQ_ERR_UNSUPPORTED;  // units are counted in 31 bits
     pl->slot_floats = (size_t)2 * pl->ctas * ru;

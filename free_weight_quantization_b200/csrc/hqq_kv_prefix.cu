@@ -22,7 +22,7 @@
 //   * eight softmax warps: two threads have a row, 32 tokens of a tile each; they read their
 //     scores from tensor memory, keep a common running maximum and a sum each, and write the
 //     weights.  O is rescaled in tensor memory only when the maximum has grown by more than 2^8, or
-//     a larger value scale appears.  (Four warps with a thread to a row: 114 us where this takes 104.)
+//     a larger value scale appears.  (Four warps with a thread to a row: 114 us a call where this took 104.)
 // The two CTAs of an SM cover each other's turns: while one's scores are in its softmax warps the
 // other's products run.
 //
