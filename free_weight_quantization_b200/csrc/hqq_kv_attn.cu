@@ -163,7 +163,7 @@ struct Shape {
     static constexpr int kCodeBytes = kBlock * kRowBytes, kMetaBytes = kBlock * NG * 4;
     static constexpr int kStage = 2 * (kCodeBytes + kMetaBytes);  // keys, values, their metadata
     // blocks in flight: some 8 KB for each warp
-    static constexpr int kStages = kStage >= 6144 ? 2 : kStage >= 3072 ? 3 : kStage >= 1536 ? 4 : 6;
+    static constexpr int kStages = kStage >= 6144 ? 2 : kStage > 2560 ? 3 : kStage >= 1536 ? 4 : 6;
     static constexpr int kRow = D + 4;  // floats of a row of results: 16-byte stores, two to a bank
     static constexpr int kRing = kAttnWarps * kStages * kStage;
     static constexpr int kResult = kAttnWarps * 8 * RB * (kRow + 2) * 4;
