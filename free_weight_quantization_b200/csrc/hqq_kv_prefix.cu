@@ -59,8 +59,8 @@ struct TcShape {
     static constexpr int kMeta = NG * kTcTokens * 4 + 16;  // ks; valid[2], the values' unit of each group
     static constexpr int kZq0 = kQ, kStage0 = kZq0 + NG * kZqG, kZk0 = kStage0 + 4 * kTile, kZero0 = kZk0 + 2 * NG * kZkG;
     static constexpr int kMeta0 = kZero0 + kZero;
-    static constexpr int kTops0 = kMeta0 + 2 * kMeta;      // [4 warps][NG]: largest value scales
-    static constexpr int kBars = kTops0 + 16 * NG;
+    static constexpr int kTops0 = kMeta0 + 2 * kMeta;      // [2 stages][4 warps][NG]: largest value scales
+    static constexpr int kBars = kTops0 + 32 * NG;
     static constexpr int kRow0 = kBars + 64;                   // [2][128] floats: what a row's two threads exchange
     static constexpr int kSmem = kRow0 + 8 * kTcRows + 1024;   // + alignment slack
     static constexpr int kOCol = NG * kTcTokens;               // O behind S in tensor memory
@@ -391,21 +391,24 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
                 page = page_of(i + 2);
             }
             float less[NG], scale[NG];
-            // the tile's largest value scale of each group: two warps hold the 64 tokens, twice
+            // the tile's largest value scale of each group: two warps hold the 64 tokens, twice.  Two
+            // buffers: a warp that is ahead writes tile i + 1's while another still reads tile i's, and
+            // it writes tile i + 2's only after all have met in tile i + 1, their reads of tile i's done
+            const uint32_t tops = base + S::kTops0 + st * (16 * NG);
 #pragma unroll
             for (int x = 0; x < NG; ++x) {
                 const float2 vm = __half22float2(*reinterpret_cast<const __half2 *>(&cur.vm[x]));
                 less[x] = vm.y + code_base<NB>();
                 scale[x] = vm.x;
                 const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(vm.x));
-                if (lane == 0) sts_u(base + S::kTops0 + ((warp & 3) * NG + x) * 4, top);
+                if (lane == 0) sts_u(tops + ((warp & 3) * NG + x) * 4, top);
             }
             asm volatile("barrier.cta.sync 5, 128;" ::: "memory");
 #pragma unroll
             for (int x = 0; x < NG; ++x) {
                 uint32_t t0, t1;
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(t0) : "r"(base + S::kTops0 + x * 4));
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(t1) : "r"(base + S::kTops0 + (NG + x) * 4));
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(t0) : "r"(tops + x * 4));
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(t1) : "r"(tops + (NG + x) * 4));
                 unit_v[x] = fmaxf(unit_v[x], __uint_as_float((max(t0, t1) + 0x007fffffu) & 0x7f800000u));
                 scale[x] *= 1.0f / unit_v[x];
             }
