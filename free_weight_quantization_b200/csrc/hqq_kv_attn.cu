@@ -890,6 +890,9 @@ int make_attn_plan(const hqq_kv_cache_t *cache, int64_t batch, int64_t nq, int64
         batch * nq > INT32_MAX / heads)
         return HQQ_ERR_UNSUPPORTED;
     *pl = AttnPlan{};
+    // a window of max_len tokens hides none; below it, sums with nq stay far within 64 bits
+    if (window >= max_len) window = 0;
+    pl->window = window;
     if (batch * nq == 0) return HQQ_OK;  // no rows: nothing is launched
     const int64_t rows = nq * (heads / c.heads);
     const int ru = pl->pair_rows = rows_per_cta(cache->head_dim, rows);
@@ -1053,7 +1056,7 @@ extern "C" int hqq_kv_attention(const hqq_kv_cache_t *cache, const void *q, int 
     a.pages_stride = pages_stride;
     a.lens = lens;
     a.max_len = max_len;
-    a.window = window;
+    a.window = pl.window;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.out = (uint16_t *)out;
     a.lse = lse;

@@ -22,7 +22,7 @@ struct Attn {
     int64_t pages_stride;
     const int32_t *lens;               // [batch]
     int64_t max_len;
-    int64_t window;                    // 0: none
+    int64_t window;                    // 0: none; below max_len
     const int32_t *prefix_pages;       // of the prefix that every sequence shares
     int64_t prefix_len;
     float scale_log2;                  // softmax scale * log2(e)
@@ -45,6 +45,7 @@ struct AttnPlan {
     int64_t prefix_chunk;
     int ctas, pair_rows, row_blocks, prefix_splits, prefix_row_blocks;
     bool prefix_tc;  // the prefix by hqq_kv_prefix_tc_kernel
+    int64_t window;  // 0 where it hides nothing
     size_t part_floats, slot_floats, bytes;
 };
 

@@ -451,6 +451,8 @@ def _kv_attend(cache: KVCache, q, pages, lens, prefix, window, scale, max_len, o
         raise HqqError("max_len must lie between 0 and max_pages * page_size")
     if window < 0:
         raise HqqError("window must not be negative (0: none)")
+    if window >= max_len:
+        window = 0  # hides nothing, and need not fit the call's 64 bits
     if scale is None:
         scale = dim ** -0.5
     prefix_len = 0

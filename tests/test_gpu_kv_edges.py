@@ -1,9 +1,11 @@
 """The key/value cache's calls at the ends of their ranges, against the 64-bit forms and the tolerances
 of test_gpu_kv.py."""
+import sys
+
 import numpy as np
 import pytest
 
-from test_gpu_kv import F16, bits, check, context, hqq, random_cache  # noqa: F401
+from test_gpu_kv import F16, attend, bits, check, context, hqq, random_cache, tables_of  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +57,24 @@ def test_prefix_value_scales_grow(hqq, D, g, nb):  # noqa: F811
     for _ in range(20):
         again, lse2 = run()
         assert torch.equal(bits(again), bits(out)) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("lens", [[4000, 3, 700], [600, 1]])
+def test_windows_that_hide_nothing(hqq, lens):  # noqa: F811
+    # one plan with shared CTAs, one with a CTA a pair; "no limit" as a number, up to the largest
+    rng = np.random.default_rng(len(lens))
+    ps, kv, heads, D = 64, 2, 8, 128
+    wide = -(-max(lens) // ps)
+    pages = sum(-(-n // ps) for n in lens)
+    cache = random_cache(hqq, rng, pages, kv, D, ps, 4, 64)
+    t = tables_of(rng, pages, lens, ps, wide)
+    q = torch.from_numpy(rng.standard_normal((len(lens), 3, heads, D)).astype(np.float32)).cuda().to(F16)
+    tc, lc = torch.from_numpy(t).cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    want = hqq.hqq_kv_attention(cache, q, tc, lc, return_lse=True)
+    check(*want, attend(cache, q.float().cpu().numpy(), t, lens))
+    for window in (wide * ps, 2 ** 31 - 1, 2 ** 31, sys.maxsize - 20, sys.maxsize, 2 ** 64 + 5):
+        got = hqq.hqq_kv_attention(cache, q, tc, lc, window=window, return_lse=True)
+        assert torch.equal(bits(got[0]), bits(want[0])) and torch.equal(got[1], want[1]), window
+    for window in (wide * ps - 1, max(lens) - 1):   # the largest that hide something, or might
+        got = hqq.hqq_kv_attention(cache, q, tc, lc, window=window, return_lse=True)
+        check(*got, attend(cache, q.float().cpu().numpy(), t, lens, window))

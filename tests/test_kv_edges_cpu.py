@@ -1,0 +1,19 @@
+"""The key/value cache's plans and refusals at the ends of their ranges.  No GPU is needed."""
+import ctypes
+
+import pytest
+
+from test_kv_cpu import L, cache  # noqa: F401
+
+pytest.importorskip("torch")
+
+
+@pytest.mark.parametrize("batch,nq,max_len", [(4, 1, 8192), (1, 1, 100000), (64, 7, 2048), (3, 2, 600), (1, 65535, 5000),
+                                              (1, 1, 2 ** 31 - 1)])
+def test_a_window_that_hides_nothing_is_planned_as_none(L, batch, nq, max_len):  # noqa: F811
+    c = cache(heads=8)
+    ws = lambda window: L.hqq_kv_attention_workspace_bytes(ctypes.byref(c), batch, nq, 32, max_len, window, 0)  # noqa: E731
+    none = ws(0)
+    assert none > 0 or max_len <= 1024
+    for window in (max_len, max_len + 1, 2 ** 31 - 1, 2 ** 31, 2 ** 63 - 17 - nq, 2 ** 63 - 17, 2 ** 63 - 16, 2 ** 63 - 2, 2 ** 63 - 1):
+        assert ws(window) == none, window
