@@ -356,23 +356,27 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
     float *rows_unit = rows_sum + RU * NG;                                     // [RU]
     int *rows_lo = reinterpret_cast<int *>(rows_unit + RU), *rows_hi = rows_lo + RU;  // visible tokens from `from`
     {
-        float x[E], big = 0.0f;
+        float x[E];
+        uint32_t big = 0;  // the bits of the largest magnitude: of infinities and NaN 0x7f800000 and above
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const uint32_t w = live ? raw[e / 2] : 0u;
             x[e] = a.bf ? __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16) : to_f32<false>((uint16_t)(e & 1 ? w >> 16 : w));
-            big = fmaxf(big, fabsf(x[e]));
+            big = max(big, __float_as_uint(fabsf(x[e])));
         }
 #pragma unroll
-        for (int y = 1; y < T; y *= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, y));
+        for (int y = 1; y < T; y *= 2) big = max(big, __shfl_xor_sync(0xffffffffu, big, y));
         // 2^(14 - floor(log2 big)); both it and its inverse stay normal
-        const int ex = big > 0.0f ? min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 100) : 0;
+        const int ex = big > 0 ? min(max((int)(big >> 23) - 127, -100), 100) : 0;
         const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+        // a row with an infinity or a NaN becomes NaN in every product: its score of each token that it
+        // sees is NaN, and its result (an infinite score would look like a hidden token)
+        const float by = big < 0x7f800000u ? up : __uint_as_float(0x7fc00000u);
         float sum = 0.0f;
         __half *to_q = reinterpret_cast<__half *>(rows_q);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            x[e] *= up;
+            x[e] *= by;
             sum += x[e];
             const int d = d0 + e, run = d % g / (g / 4), code = d / g * (g / 4) + d % (g / 4);
             const int reg = code / (2 * KRegs::kSpan) * KRegs::kSpan + code % KRegs::kSpan;
@@ -676,8 +680,9 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
             acc[2] = __fmaf_rn(v.z, f, acc[2]);
             acc[3] = __fmaf_rn(v.w, f, acc[3]);
         }
-        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-        const float lse = sum > 0.0f ? top + log2f(sum) : -INFINITY;
+        // a sum of zero is a row that sees nothing; a NaN stays
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float lse = sum == 0.0f ? -INFINITY : top + log2f(sum);
         const int64_t orow = out_row(row0 + rr);
         if (part_o) {
             const int64_t at = by_slot ? rr : orow;
@@ -862,9 +867,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) hqq_kv_join_kernel(const Attn
             y += acc_s[w][d];
             z += sum_s[w];
         }
-        y = z > 0.0f ? y / z : 0.0f;
+        y = z == 0.0f ? 0.0f : y / z;  // zero: the row sees nothing; a NaN, of a part too, stays
         a.out[row * D + d] = a.bf ? from_f32<true>(y) : from_f32<false>(y);
-        if (d == 0 && a.lse) a.lse[row] = z > 0.0f ? (top + log2f(z)) * 0.6931471805599453f : -INFINITY;
+        if (d == 0 && a.lse) a.lse[row] = z == 0.0f ? -INFINITY : (top + log2f(z)) * 0.6931471805599453f;
     }
 }
 

@@ -277,21 +277,23 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
                     raw[2 * e + 1] = __ldg(q + 4 * e + 2) | (uint32_t)__ldg(q + 4 * e + 3) << 16;
                 }
             }
-            float v[8], big = 0.0f, sum = 0.0f;
+            float v[8], sum = 0.0f;
+            uint32_t big = 0;  // the bits of the largest magnitude
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const uint32_t w = there ? raw[e / 2] : 0u;
                 v[e] = a.bf ? __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16) : to_f32<false>((uint16_t)(e & 1 ? w >> 16 : w));
-                big = fmaxf(big, fabsf(v[e]));
+                big = max(big, __float_as_uint(fabsf(v[e])));
             }
 #pragma unroll
-            for (int x = 1; x < T; x *= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
-            const int ex = big > 0.0f ? min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 100) : 0;
+            for (int x = 1; x < T; x *= 2) big = max(big, __shfl_xor_sync(0xffffffffu, big, x));
+            const int ex = big > 0 ? min(max((int)(big >> 23) - 127, -100), 100) : 0;
             const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+            const float by = big < 0x7f800000u ? up : __uint_as_float(0x7fc00000u);  // an infinity or a NaN: a row of NaN
             __half y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                v[e] *= up;
+                v[e] *= by;
                 sum += v[e];
                 y[place<NB>(e)] = __float2half_rn(v[e] * (1.0f / (float)(1 << place_up<NB>(e))));
             }
@@ -626,9 +628,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
         meet_pair(pair);
         float other;
         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(row_at + (hf ^ 1) * kTcRows * 4));
-        ok = ok && other >= 0.0f;
+        ok = ok && !(other < 0.0f);
         const float sum = l2.x + l2.y + other;
-        const float f = !ok ? __int_as_float(0x7fc00000) : sum > 0.0f ? vref[NG == 1 ? 0 : hf] / sum : 0.0f;
+        const float f = !ok ? __int_as_float(0x7fc00000) : sum == 0.0f ? 0.0f : vref[NG == 1 ? 0 : hf] / sum;
         // by way of shared memory (everything there has been read), so that a row goes out in one piece:
         // rows 16 bytes more than D floats apart, which meet in no bank
         constexpr uint32_t kRow = D * 4 + 16;
@@ -644,7 +646,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
                 const int d = grp * g + in_g / (g / 64) * (g / 8) + in_g % (g / 64) * 8;
                 uint32_t y[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = sum > 0.0f || !ok ? __float_as_uint(x[8 * k + place<NB>(e)] * f) : 0u;
+                for (int e = 0; e < 8; ++e) y[e] = sum != 0.0f || !ok ? __float_as_uint(x[8 * k + place<NB>(e)] * f) : 0u;
                 sts16(base + (uint32_t)lrow * kRow + d * 4, make_uint4(y[0], y[1], y[2], y[3]));
                 sts16(base + (uint32_t)lrow * kRow + d * 4 + 16, make_uint4(y[4], y[5], y[6], y[7]));
             }
@@ -657,7 +659,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
             if (lane < D / 4)
                 *reinterpret_cast<float4 *>(a.part_o + (split * rows + to_row) * D + 4 * lane) = lds_f4(base + (uint32_t)rr * kRow + 16 * lane);
         }
-        if (live && hf == 0) a.part_lse[split * rows + orow] = !ok ? f : sum > 0.0f ? m - kUp + log2f(sum) : -INFINITY;
+        if (live && hf == 0) a.part_lse[split * rows + orow] = !ok ? f : sum == 0.0f ? -INFINITY : m - kUp + log2f(sum);
     }
     fence_before();
     __syncthreads();

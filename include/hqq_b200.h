@@ -288,7 +288,7 @@ size_t hqq_kv_attention_workspace_bytes(const hqq_kv_cache_t *cache, int64_t bat
  * largest), once for codes and zero points alike.
  *   q         [batch][nq][heads][head_dim], 2-byte aligned, with the given strides (in values);
  *             heads a multiple of kv_heads, query head h reads key head h / (heads / kv_heads).
- *             Finite values; a row with an infinity or a NaN has an unspecified result
+ *             A row with an infinity or a NaN that sees a token comes back as NaN, out and lse
  *   pages     [batch][max_pages] device int32, rows pages_stride apart: each sequence's pages in
  *             order.  Tokens of a page number outside the pool are not seen
  *   lens      [batch] device int32: tokens of each sequence, the queries' own among them (append

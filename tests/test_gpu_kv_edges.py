@@ -5,7 +5,7 @@ import sys
 import numpy as np
 import pytest
 
-from test_gpu_kv import F16, attend, bits, check, context, hqq, random_cache, tables_of  # noqa: F401
+from test_gpu_kv import BF16, F16, attend, bits, check, context, hqq, random_cache, tables_of  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +78,47 @@ def test_windows_that_hide_nothing(hqq, lens):  # noqa: F811
     for window in (wide * ps - 1, max(lens) - 1):   # the largest that hide something, or might
         got = hqq.hqq_kv_attention(cache, q, tc, lc, window=window, return_lse=True)
         check(*got, attend(cache, q.float().cpu().numpy(), t, lens, window))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("path", ["own", "shared", "prefix", "many rows"])
+def test_a_row_that_is_not_finite_is_nan(hqq, path, dtype):  # noqa: F811
+    # on every path (one CTA a pair, cut pairs, a prefix of few rows, of many): such a row is NaN where it
+    # sees a token, and the other rows are what they are beside finite rows.  Without zero points an infinity in q makes every
+    # score the same infinity, which must not look like a hidden token
+    rng = np.random.default_rng(5)
+    D, ps, kv, heads = 128, 16, 2, 8
+    lens = {"shared": [2500, 1, 700, 40], "own": [500, 1, 30, 40]}.get(path, [30, 1, 70, 4])
+    B, nq = len(lens), 10 if path == "many rows" else 3
+    shared = -(-333 // ps) if path not in ("own", "shared") else 0
+    pages = shared + sum(-(-n // ps) for n in lens)
+    cache = random_cache(hqq, rng, pages, kv, D, ps, 8, 64)
+    cache.k_meta[..., 1] = 0
+    t = tables_of(rng, pages - shared, lens, ps, -(-max(lens) // ps)) + shared
+    tc, lc = torch.from_numpy(t.astype(np.int32)).cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    pt = torch.from_numpy(rng.permutation(shared).astype(np.int32)).cuda()
+
+    def run(x):
+        if shared:
+            return hqq.hqq_kv_prefix_attention(cache, x, pt, 333, tc, lc, return_lse=True)
+        return hqq.hqq_kv_attention(cache, x, tc, lc, return_lse=True)
+    q = torch.from_numpy(rng.standard_normal((B, nq, heads, D)).astype(np.float32)).cuda().to(dtype)
+    want, lse = run(q)
+    assert torch.isfinite(want).all()
+    bad, x = torch.zeros(B, nq, heads, dtype=torch.bool, device="cuda"), q.clone()
+    # rows (0, 0) of the sequence of one token see nothing of their own (and all but 2 of a prefix)
+    for (b, i, h), d, what in (((0, 0, 0), 3, np.nan), ((0, nq - 1, 5), 127, np.inf), ((2, 1, 2), 64, -np.inf), ((3, 2, 7), 0, np.nan),
+                               ((3, 0, 4), 1, -np.inf), ((1, nq - 1, 3), 9, np.inf), ((1, 0, 1), 70, np.nan), ((2, 2, 6), 0, np.inf)):
+        x[b, i, h, d] = what
+        bad[b, i, h] = True
+    x[2, 2, 6, 1] = -np.inf      # both infinities
+    x[0, 0, 1], bad[0, 0, 1] = np.nan, True
+    got, lse2 = run(x)
+    sees = ~torch.isinf(lse)
+    assert (bad & ~sees).any() == (not shared)
+    assert torch.isnan(got[bad & sees]).all() and torch.isnan(lse2[bad & sees]).all()
+    # The others to their tolerance, not to the bit: the rows of a block move their running maxima together,
+    # when any of them asks for it, and a weight exp(s - m) is rounded to fp16 whatever m is, so that a
+    # row's last bit depends on when the rows beside it asked.  A NaN asks for nothing.
+    got[bad & sees], lse2[bad & sees] = want[bad & sees], lse[bad & sees]
+    check(got, lse2, attend(cache, q.float().cpu().numpy(), t, lens, prefix=(pt.cpu().numpy(), 333) if shared else (None, 0)))
