@@ -439,8 +439,11 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
             l[rb][y] = 0.0f;
         }
     }
-    float vref = 0x1p-24f;    // a power of two, at least every value scale so far
-    float vin = kWeightUnit * 0x1p24f;
+    // what a group's value scales are multiplied by: kWeightUnit over a power of two that is at least
+    // every scale of the group so far, so that its weights lie within fp16 whatever the others' scales are
+    float vin[NG];
+#pragma unroll
+    for (int x = 0; x < NG; ++x) vin[x] = kWeightUnit * 0x1p24f;
 
     const uint32_t k_at = pinned(16 * key_chunk(n, r, j * kKeyBytes / 16) + j * kKeyBytes % 16);
     // the odd lanes read the second token of a pair first
@@ -561,26 +564,32 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
             }
         }
         // ---- a new maximum, or a larger value scale than any before: rescale
-        __half2 vs2 = __float2half2_rn(0.0f);
+        float vw[NG][2], most = 0.0f;
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+        for (int x = 0; x < NG; ++x)
 #pragma unroll
-            for (int x = 0; x < NG; ++x) vs2 = __hmax2(vs2, *reinterpret_cast<const __half2 *>(&vm[y][x]));
-        const float vs = __low2float(vs2);
-        bool more = vs > vref;
+            for (int y = 0; y < 2; ++y) {
+                vw[x][y] = __low2float(*reinterpret_cast<const __half2 *>(&vm[y][x])) * vin[x];
+                most = fmaxf(most, vw[x][y]);
+            }
+        bool more = most > kWeightUnit;
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
             for (int y = 0; y < 2; ++y) more |= fmaxf(s[rb][y], s[rb][y + 2]) > bound[rb][y];
         if (__any_sync(0xffffffffu, more)) {
-            float big = vs;
+            float fv[NG];
 #pragma unroll
-            for (int x = 16; x > 0; x /= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
-            // the power of two at or above it
-            const float up = fmaxf(vref, __uint_as_float((__float_as_uint(big) + 0x007fffffu) & 0x7f800000u));
-            const float fv = vref / up;
-            vref = up;
-            vin = kWeightUnit / up;
+            for (int x = 0; x < NG; ++x) {
+                // a new unit has room for scales four times as large, so that few blocks ask for one
+                const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vw[x][0], vw[x][1])));
+                // kWeightUnit / 4 over the power of two at or above big
+                const uint32_t less = __float_as_uint(kWeightUnit / 4.0f) + (127u << 23) - ((big + 0x007fffffu) & 0x7f800000u);
+                fv[x] = big > __float_as_uint(kWeightUnit) ? __uint_as_float(less) : 1.0f;
+                vin[x] *= fv[x];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) vw[x][y] *= fv[x];
+            }
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb) {
                 float f[2];
@@ -594,14 +603,13 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
                     m[rb][y] = top;
                     bound[rb][y] = top == kLowest ? -INFINITY : (top + kLag) / unit[rb][y];
                     l[rb][y] *= f[y];
-                    f[y] *= fv;
                 }
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
 #pragma unroll
-                    for (int x = 0; x < VR / 2; ++x) o[rb][x][y] *= f[y & 1];
+                    for (int x = 0; x < VR / 2; ++x) o[rb][x][y] *= f[y & 1] * fv[x / (g / 16)];
 #pragma unroll
-                    for (int x = 0; x < NG; ++x) oz[rb][x][y] *= f[y & 1];
+                    for (int x = 0; x < NG; ++x) oz[rb][x][y] *= f[y & 1] * fv[x];
                 }
             }
         }
@@ -618,12 +626,11 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
         for (int x = 0; x < NG; ++x)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                const float vw = __low2float(*reinterpret_cast<const __half2 *>(&vm[y][x])) * vin;
                 // a column of the tokens' zero points, alike for all 16 rows of an operand
                 z[x][y] = turn(__byte_perm(vm[y][x], 0, 0x3232));
 #pragma unroll
                 for (int rb = 0; rb < RB; ++rb) {
-                    const __half2 h = __floats2half2_rn(p[rb][2 * y] * vw, p[rb][2 * y + 1] * vw);
+                    const __half2 h = __floats2half2_rn(p[rb][2 * y] * vw[x][y], p[rb][2 * y + 1] * vw[x][y]);
                     w[rb][x][y] = turn(*reinterpret_cast<const uint32_t *>(&h));
                 }
             }
@@ -646,11 +653,11 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
                 res_l[warp * RU + 8 * rb + 2 * j + y] = l[rb][y];
             }
         }
-        const float vu = vref / kWeightUnit;
         constexpr int s8 = g / 8;
 #pragma unroll
         for (int x = 0; x < VR; x += 4) {  // s8 is 4 or more: four elements in a row
             const int d = x / s8 * g + r * s8 + x % s8;
+            const float vu = __uint_as_float(0x7f000000u - __float_as_uint(vin[x / s8]));  // 1 over a power of two
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 float e[4];

@@ -51,9 +51,9 @@ struct AttnPlan {
 
 constexpr float kLowest = -1e30f;  // a maximum before any score
 // The running maximum may lag behind by this many powers of two before the sums are rescaled:
-// weights stay below 2^8 of what they are relative to.  w is kept within fp16 by 2^6 * 2^8 < 65504.
+// weights stay below 2^8 of what they are relative to.  w is kept within fp16 by 2^7 * 2^8 < 65504.
 constexpr float kLag = 8.0f;
-constexpr float kWeightUnit = 64.0f;
+constexpr float kWeightUnit = 128.0f;
 
 // A 32-bit word holds codes in two halves that an operand register takes side by side.  Code u of
 // byte h of the halves is brought to bit up(u): as high as it can be below the fp16 exponent at

@@ -122,3 +122,30 @@ def test_a_row_that_is_not_finite_is_nan(hqq, path, dtype):  # noqa: F811
     # row's last bit depends on when the rows beside it asked.  A NaN asks for nothing.
     got[bad & sees], lse2[bad & sees] = want[bad & sees], lse[bad & sees]
     check(got, lse2, attend(cache, q.float().cpu().numpy(), t, lens, prefix=(pt.cpu().numpy(), 333) if shared else (None, 0)))
+
+
+@pytest.mark.parametrize("apart", [14, 20])
+@pytest.mark.parametrize("path", ["own", "shared", "prefix", "many rows"])
+@pytest.mark.parametrize("D,nb,g", [(128, 4, 64), (128, 2, 32), (256, 8, 32), (64, 4, 32)])
+def test_groups_of_far_apart_value_scales(hqq, D, nb, g, path, apart):  # noqa: F811
+    # the groups of a value keep their accuracy beside one whose scales are 2^14 or 2^20 larger, for tokens
+    # of small weight too (scores spread over some 2^20): each group has a unit of its own
+    rng = np.random.default_rng(D + nb + apart)
+    ps, kv, heads = 16, 2, 8
+    lens = {"shared": [2500, 700], "own": [500, 30]}.get(path, [30, 1, 70, 4])
+    B, nq = len(lens), 10 if path == "many rows" else 1
+    prefix = 700 if path not in ("own", "shared") else 0
+    shared = -(-prefix // ps)
+    pages = shared + sum(-(-n // ps) for n in lens)
+    cache = random_cache(hqq, rng, pages, kv, D, ps, nb, g)
+    up = torch.arange(D // g, device="cuda") % 2 * apart - apart + 9.0
+    cache.v_meta[..., 0] = (cache.v_meta[..., 0].float() * 2.0 ** up).clamp(2.0 ** -24, 2.0 ** 15).half()
+    t = tables_of(rng, pages - shared, lens, ps, -(-max(lens) // ps)) + shared
+    tc, lc = torch.from_numpy(t.astype(np.int32)).cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    pt = rng.permutation(shared).astype(np.int32)
+    q = torch.from_numpy((3 * rng.standard_normal((B, nq, heads, D))).astype(np.float32)).cuda().to(BF16)
+    if shared:
+        out, lse = hqq.hqq_kv_prefix_attention(cache, q, torch.from_numpy(pt).cuda(), prefix, tc, lc, return_lse=True)
+    else:
+        out, lse = hqq.hqq_kv_attention(cache, q, tc, lc, return_lse=True)
+    check(out, lse, attend(cache, q.float().cpu().numpy(), t, lens, prefix=(pt, prefix) if shared else (None, 0)))
