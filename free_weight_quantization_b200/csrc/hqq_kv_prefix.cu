@@ -414,7 +414,10 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
                 unit_v[x] = fmaxf(unit_v[x], __uint_as_float((max(t0, t1) + 0x007fffffu) & 0x7f800000u));
                 scale[x] *= 1.0f / unit_v[x];
             }
-            if (i >= 2 && ok) ok = wait_for(kv_free + 8 * st, (uint32_t)((i >> 1) - 1) & 1u);
+            if (i >= 2 && ok) {
+                ok = wait_for(kv_free + 8 * st, (uint32_t)((i >> 1) - 1) & 1u);
+                if (!ok) failed = 1;  // before this tile is handed over: who sees its products sees it
+            }
             const uint32_t kt = base + S::kStage0 + st * 2 * S::kTile, vt = kt + S::kTile, mt = base + S::kMeta0 + st * S::kMeta;
 #pragma unroll
             for (int x = 0; x < CH / 2; ++x) {
@@ -459,7 +462,6 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
                 page = page_of(i + 2);
             }
         }
-        if (!ok) failed = 1;
     } else if (role == 3) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
         if (warp == 12 && elected()) {
@@ -620,7 +622,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
             mbar_arrive(p_full);
         }
         // ---- the chunk's result, normalised by itself: half of the elements each
-        if (ok) ok = wait_for(done, 0u);
+        // (also where a wait ran out: the products in flight read shared memory and write tensor memory)
+        if (!wait_for(done, 0u)) ok = false;
         ok = ok && !failed;
         fence_after();
         meet_pair(pair);  // the other's maximum has been read
