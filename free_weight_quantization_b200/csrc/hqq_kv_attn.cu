@@ -357,7 +357,7 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
     int *rows_lo = reinterpret_cast<int *>(rows_unit + RU), *rows_hi = rows_lo + RU;  // visible tokens from `from`
     {
         float x[E];
-        uint32_t big = 0;  // the bits of the largest magnitude: of infinities and NaN 0x7f800000 and above
+        uint32_t big = 0;  // the bits of the largest magnitude; a NaN's are above any number's
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const uint32_t w = live ? raw[e / 2] : 0u;
@@ -369,9 +369,9 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
         // 2^(14 - floor(log2 big)); both it and its inverse stay normal
         const int ex = big > 0 ? min(max((int)(big >> 23) - 127, -100), 100) : 0;
         const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
-        // a row with an infinity or a NaN becomes NaN in every product: its score of each token that it
-        // sees is NaN, and its result (an infinite score would look like a hidden token)
-        const float by = big < 0x7f800000u ? up : __uint_as_float(0x7fc00000u);
+        // a row with an infinity, a NaN or numbers out of range becomes NaN in every product: its score of
+        // each token that it sees is NaN, and its result (an infinite score would look like a hidden token)
+        const float by = row_in_range(big, a.scale_log2) ? up : __uint_as_float(0x7fc00000u);
         float sum = 0.0f;
         __half *to_q = reinterpret_cast<__half *>(rows_q);
 #pragma unroll
@@ -395,7 +395,7 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
             const int64_t cap = to - from;
             rows_hi[rr] = live ? (int)min(max(hi - from, (int64_t)0), cap) : (int)cap;
             rows_lo[rr] = live ? (int)min(max(lo - from, (int64_t)0), cap) : 0;
-            rows_unit[rr] = 0x1p24f / up * a.scale_log2;
+            rows_unit[rr] = row_unit(up, a.scale_log2);
         }
     }
     __syncthreads();
@@ -602,7 +602,7 @@ __device__ __forceinline__ void attend_segment(const Attn &a, int b0, int row0, 
                     f[y] = exp2_fast(m[rb][y] - top);
                     m[rb][y] = top;
                     bound[rb][y] = top == kLowest ? -INFINITY : (top + kLag) / unit[rb][y];
-                    l[rb][y] *= f[y];
+                    l[rb][y] *= score_in_range(top) ? f[y] : __uint_as_float(0x7fc00000u);
                 }
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
@@ -885,6 +885,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) hqq_kv_join_kernel(const Attn
 // 64 rows 25 / 22, 128 rows 27 / 30; 32768 tokens 32 rows 57 / 39, 64 rows 58 / 59.
 constexpr int kTcMinRows = 64;
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // rows that a CTA takes: 8, or 16 where a key head has more (and the accumulators fit)
@@ -998,7 +1000,7 @@ int check_attention(const hqq_kv_cache_t *cache, const void *q, int dtype, int64
                     const int32_t *pages, int64_t max_pages, const int32_t *lens, int64_t max_len, float scale,
                     void *out, float *lse, void *workspace, size_t workspace_bytes, const AttnPlan &pl) {
     if (dtype != HQQ_FP16 && dtype != HQQ_BF16) return HQQ_ERR_ARG;
-    if (max_pages < 0 || max_len > max_pages * (int64_t)cache->page_size || !(scale > 0.0f) || !std::isfinite(scale))
+    if (max_pages < 0 || max_len > max_pages * (int64_t)cache->page_size || !(scale > 0.0f) || !std::isfinite(scale * kLog2e))
         return HQQ_ERR_ARG;
     if (batch == 0 || nq == 0) return HQQ_OK;
     if (!q || !lens || !out || (max_pages > 0 && !pages)) return HQQ_ERR_ARG;
@@ -1069,7 +1071,7 @@ extern "C" int hqq_kv_attention(const hqq_kv_cache_t *cache, const void *q, int 
     a.lens = lens;
     a.max_len = max_len;
     a.window = pl.window;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = scale * kLog2e;
     a.out = (uint16_t *)out;
     a.lse = lse;
     a.bf = dtype == HQQ_BF16;
@@ -1108,7 +1110,7 @@ extern "C" int hqq_kv_prefix_attention(const hqq_kv_cache_t *cache, const void *
     a.max_len = max_len;
     a.prefix_pages = prefix_pages;
     a.prefix_len = prefix_len;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = scale * kLog2e;
     a.out = (uint16_t *)out;
     a.lse = lse;
     a.bf = dtype == HQQ_BF16;

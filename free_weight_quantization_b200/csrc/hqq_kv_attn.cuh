@@ -49,7 +49,23 @@ struct AttnPlan {
     size_t part_floats, slot_floats, bytes;
 };
 
-constexpr float kLowest = -1e30f;  // a maximum before any score
+// A query row that the products can take: below 2^100, so that one power of two brings it into fp16,
+// and, in units of the scores, below 2^84: D (255 + |zero|) scale of a key is below 2^40, so that
+// every score lies above kLowest.  Any other row is made NaN.  big: the bits of its largest magnitude.
+constexpr float kLowest = -0x1p126f;  // a maximum before any score
+__device__ __forceinline__ bool row_in_range(uint32_t big, float scale_log2) {
+    return big < (227u << 23) && __uint_as_float(big) * scale_log2 < 0x1p84f;
+}
+
+// The largest score, in powers of two, of a row that can be answered: exp2(s unit - m) takes the
+// rounding of m = max(s) unit to the exponent, 2^-24 of the score.  Beyond, the row is made NaN.
+constexpr float kScoreLimit = 0x1p22f;
+__device__ __forceinline__ bool score_in_range(float top) { return fabsf(top) < kScoreLimit || top == kLowest; }
+
+// What a row's raw scores, of q * up and codes * 2^-24, are multiplied by.  Not 0, by which a hidden
+// token's -infinity would become NaN.
+__device__ __forceinline__ float row_unit(float up, float scale_log2) { return fmaxf(0x1p24f / up * scale_log2, 0x1p-126f); }
+
 // The running maximum may lag behind by this many powers of two before the sums are rescaled:
 // weights stay below 2^8 of what they are relative to.  w is kept within fp16 by 2^7 * 2^8 < 65504.
 constexpr float kLag = 8.0f;

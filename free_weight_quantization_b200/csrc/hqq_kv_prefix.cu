@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
             for (int x = 1; x < T; x *= 2) big = max(big, __shfl_xor_sync(0xffffffffu, big, x));
             const int ex = big > 0 ? min(max((int)(big >> 23) - 127, -100), 100) : 0;
             const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
-            const float by = big < 0x7f800000u ? up : __uint_as_float(0x7fc00000u);  // an infinity or a NaN: a row of NaN
+            const float by = row_in_range(big, a.scale_log2) ? up : __uint_as_float(0x7fc00000u);  // out of range: a row of NaN
             __half y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
                 const __half2 two = __halves2half2(top, rest);
                 sts_u(base + S::kZq0 + d / g * S::kZqG + rr * 16, *reinterpret_cast<const uint32_t *>(&two));
             }
-            if (d == 0) sts_f(base + S::kMeta0 + rr * 4, 0x1p24f / up * a.scale_log2);  // until the tiles come
+            if (d == 0) sts_f(base + S::kMeta0 + rr * 4, row_unit(up, a.scale_log2));  // until the tiles come
         }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -591,8 +591,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) hqq_kv_prefix_tc_kernel(const A
                 }
                 m = top;
                 bound = top == kLowest ? -INFINITY : (top + kLag) / unit;
-                l2.x *= f;
-                l2.y *= f;
+                const float fl = score_in_range(top) ? f : __uint_as_float(0x7fc00000u);
+                l2.x *= fl;
+                l2.y *= fl;
                 if (i > 0) {  // the products up to tile i - 1 have completed: S of tile i came after them
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {

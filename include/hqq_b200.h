@@ -288,13 +288,15 @@ size_t hqq_kv_attention_workspace_bytes(const hqq_kv_cache_t *cache, int64_t bat
  * largest), once for codes and zero points alike.
  *   q         [batch][nq][heads][head_dim], 2-byte aligned, with the given strides (in values);
  *             heads a multiple of kv_heads, query head h reads key head h / (heads / kv_heads).
- *             A row with an infinity or a NaN that sees a token comes back as NaN, out and lse
+ *             A row with a NaN, a magnitude of 2^100 or more or of 2^84 / (scale log2 e) or more, or
+ *             a largest score (scale log2 e q . k_t) of magnitude 2^22 or more comes back as NaN, out
+ *             and lse, if it sees a token
  *   pages     [batch][max_pages] device int32, rows pages_stride apart: each sequence's pages in
  *             order.  Tokens of a page number outside the pool are not seen
  *   lens      [batch] device int32: tokens of each sequence, the queries' own among them (append
  *             them first).  Below 0 counts as 0, above max_len as max_len
  *   max_len   at most max_pages * page_size: an upper bound on lens, which plans the launch
- *   scale     > 0
+ *   scale     > 0, and scale log2 e finite
  *   out       [batch][nq][heads][head_dim] of dtype, 16-byte aligned (output)
  *   lse       [batch][nq][heads] binary32, nullable (output)
  *   workspace >= hqq_kv_attention_workspace_bytes(..) bytes, 16-byte aligned; contents on entry do

@@ -149,3 +149,40 @@ def test_groups_of_far_apart_value_scales(hqq, D, nb, g, path, apart):  # noqa: 
     else:
         out, lse = hqq.hqq_kv_attention(cache, q, tc, lc, return_lse=True)
     check(out, lse, attend(cache, q.float().cpu().numpy(), t, lens, prefix=(pt, prefix) if shared else (None, 0)))
+
+
+@pytest.mark.parametrize("path", ["own", "shared", "prefix", "many rows"])
+@pytest.mark.parametrize("big,scale,nan", [
+    (2.0 ** 99, 2.0 ** -97, False), (2.0 ** 13, 1.0, False), (2.0 ** 40, 1.0, True), (2.0 ** 60, 1.0, True), (2.0 ** 101, 2.0 ** -99, True), (2.0 ** 90, 1.0, True),
+    (2.0 ** 110, 0.1, True), (1e-20, 1e-30, False), (2.0 ** -120, 2.0 ** -140, False), (1e-30, 2e33, False)])
+def test_range_of_queries_and_scales(hqq, path, big, scale, nan):  # noqa: F811
+    # rows as large and as small as bf16 has them, with scales that bring the scores to some units, to
+    # one-sided extremes or to nothing.  Rows out of range are NaN, never "sees nothing"
+    rng = np.random.default_rng(6)
+    D, ps, kv, heads = 64, 16, 2, 4
+    lens = {"shared": [1500, 1, 700], "own": [500, 1, 30]}.get(path, [30, 1, 70])
+    B, nq = len(lens), 14 if path == "many rows" else 3
+    prefix = 200 if path not in ("own", "shared") else 0
+    shared = -(-prefix // ps)
+    pages = shared + sum(-(-n // ps) for n in lens)
+    cache = random_cache(hqq, rng, pages, kv, D, ps, 4, 64)
+    cache.k_meta[..., 1] = 0        # keys of one sign: the scores of a row have one too
+    t = tables_of(rng, pages - shared, lens, ps, -(-max(lens) // ps)) + shared
+    tc, lc = torch.from_numpy(t.astype(np.int32)).cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    pt = rng.permutation(shared).astype(np.int32)
+    q = np.abs(rng.standard_normal((B, nq, heads, D))) / 4
+    q[:, :, 1::2] *= -1
+    q[..., 5] = np.sign(q[..., 5])  # the largest magnitude
+    q = np.clip(q, -1, 1)
+    x = torch.from_numpy((q * big).astype(np.float32)).cuda().to(BF16)
+    if shared:
+        out, lse = hqq.hqq_kv_prefix_attention(cache, x, torch.from_numpy(pt).cuda(), prefix, tc, lc, scale=scale, return_lse=True)
+    else:
+        out, lse = hqq.hqq_kv_attention(cache, x, tc, lc, scale=scale, return_lse=True)
+    want = attend(cache, x.float().cpu().numpy(), t, lens, prefix=(pt, prefix) if shared else (None, 0), scale=float(np.float32(scale)))
+    if nan:
+        sees = torch.from_numpy(np.isfinite(want[1])).cuda()
+        assert torch.isnan(out[sees]).all() and torch.isnan(lse[sees]).all()
+        assert not out[~sees].any() and torch.isneginf(lse[~sees]).all()
+    else:
+        check(out, lse, want)
