@@ -1,11 +1,12 @@
 """The key/value cache's calls at the ends of their ranges, against the 64-bit forms and the tolerances
 of test_gpu_kv.py."""
 import sys
+from types import SimpleNamespace
 
 import numpy as np
 import pytest
 
-from test_gpu_kv import BF16, F16, attend, bits, check, context, hqq, random_cache, tables_of  # noqa: F401
+from test_gpu_kv import BF16, F16, LAYOUTS, attend, bits, check, context, hqq, random_cache, tables_of  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -186,3 +187,106 @@ def test_range_of_queries_and_scales(hqq, path, big, scale, nan):  # noqa: F811
         assert not out[~sees].any() and torch.isneginf(lse[~sees]).all()
     else:
         check(out, lse, want)
+
+
+@pytest.mark.parametrize("dtype,heads", [(F16, 2), (BF16, 6)], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("D,nb,g", LAYOUTS)
+def test_layouts_on_shared_ctas(hqq, D, nb, g, dtype, heads):  # noqa: F811
+    # every layout where CTAs share the tokens: stages used again, the page table fetched again after 32
+    # blocks of a warp, pairs cut between CTAs, beside short and empty sequences
+    rng = np.random.default_rng(D * nb + g)
+    lens, ps, kv = [2200, 1, 16, 0, 130, 1025], 16, 2
+    pages = sum(-(-n // ps) for n in lens)
+    cache = random_cache(hqq, rng, pages, kv, D, ps, nb, g)
+    t = tables_of(rng, pages, lens, ps, -(-2200 // ps) + 1)
+    q = torch.from_numpy(rng.standard_normal((len(lens), 1, heads, D)).astype(np.float32)).cuda().to(dtype)
+    out, lse = hqq.hqq_kv_attention(cache, q, torch.from_numpy(t).cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), return_lse=True)
+    check(out, lse, attend(cache, q.float().cpu().numpy(), t, lens))
+
+
+@pytest.mark.parametrize("D,nb,g", [(128, 2, 64), (64, 8, 64), (256, 4, 64), (128, 4, 32)])
+def test_long_own_tokens_few_ctas(hqq, D, nb, g):  # noqa: F811
+    # many pairs of many units: each CTA has more than 32 blocks a warp of one pair
+    rng = np.random.default_rng(D + nb)
+    lens, ps, kv, heads = [int(n) for n in rng.integers(4500, 5000, 48)], 64, 8, 8
+    pages = sum(-(-n // ps) for n in lens)
+    cache = random_cache(hqq, rng, pages, kv, D, ps, nb, g)
+    t = tables_of(rng, pages, lens, ps, -(-5000 // ps))
+    q = torch.from_numpy(rng.standard_normal((len(lens), 1, heads, D)).astype(np.float32)).cuda().to(F16)
+    out, lse = hqq.hqq_kv_attention(cache, q, torch.from_numpy(t).cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), return_lse=True)
+    for b in (0, 17, 47):
+        one, own = slice(b, b + 1), torch.from_numpy(t[b, :-(-lens[b] // ps)]).long().cuda()
+        part = SimpleNamespace(**{x: getattr(cache, x) for x in ("page_size", "nbits", "group_size", "kv_heads", "head_dim")},
+                               **{x: getattr(cache, x)[own] for x in ("k_codes", "v_codes", "k_meta", "v_meta")})
+        check(out[one], lse[one], attend(part, q[one].float().cpu().numpy(), np.arange(len(own))[None], lens[one]), b)
+
+
+@pytest.mark.parametrize("nb", [2, 4, 8])
+@pytest.mark.parametrize("B,nq,heads,kv,D,g", [(3, 2, 8, 2, 128, 64), (20, 2, 8, 1, 128, 64), (18, 1, 4, 1, 64, 64),
+                                               (20, 2, 8, 1, 256, 128), (20, 2, 8, 1, 128, 32)])
+def test_prefix_and_long_own_tokens(hqq, B, nq, heads, kv, D, g, nb):  # noqa: F811
+    # the join finds the parts of pairs that are cut between CTAs and the prefix's, for both prefix kernels
+    rng = np.random.default_rng(B + D + nb)
+    ps, prefix = 32, 777
+    lens = [int(n) for n in rng.integers(0, 200, B)]
+    lens[1], lens[-1] = 1700, 1100
+    shared = -(-prefix // ps)
+    pages = shared + sum(-(-n // ps) for n in lens)
+    cache = random_cache(hqq, rng, pages, kv, D, ps, nb, g)
+    t = tables_of(rng, pages - shared, lens, ps, -(-1700 // ps)) + shared
+    pt = rng.permutation(shared).astype(np.int32)
+    q = torch.from_numpy(rng.standard_normal((B, nq, heads, D)).astype(np.float32)).cuda().to(BF16)
+    out, lse = hqq.hqq_kv_prefix_attention(cache, q, torch.from_numpy(pt).cuda(), prefix, torch.from_numpy(t.astype(np.int32)).cuda(),
+                                           torch.tensor(lens, dtype=torch.int32).cuda(), return_lse=True)
+    check(out, lse, attend(cache, q.float().cpu().numpy(), t, lens, prefix=(pt, prefix)))
+
+
+@pytest.mark.parametrize("nb,D,g", [(4, 128, 64), (2, 64, 32), (8, 256, 64)])
+def test_what_is_not_seen_does_not_matter_on_shared_ctas(hqq, nb, D, g):  # noqa: F811
+    # pages outside the pool, lengths that are cut, NaN behind the last token and before a window, with
+    # pairs that are cut between CTAs
+    rng = np.random.default_rng(nb)
+    ps, kv, heads, lens, window = 16, 2, 4, [2100, 17, 1300], 1200
+    pages = sum(-(-n // ps) for n in lens) + 5
+    t = tables_of(rng, pages, lens, ps, 140)
+    tc, lc = torch.from_numpy(t).cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    q = torch.randn(3, 1, heads, D, device="cuda").half()
+    for w in (0, window):
+        cache = random_cache(hqq, rng, pages, kv, D, ps, nb, g)
+        used = np.zeros((pages, ps), bool)
+        for b, n in enumerate(lens):
+            for tok in range(max(0, n - w) if w else 0, n):
+                used[t[b, tok // ps], tok % ps] = True
+        want = hqq.hqq_kv_attention(cache, q, tc, lc, window=w, return_lse=True)
+        check(*want, attend(cache, q.float().cpu().numpy(), t, lens, w))
+        keep = torch.from_numpy(used).cuda()[:, None, :, None, None]
+        for meta in (cache.k_meta, cache.v_meta):
+            meta.copy_(torch.where(keep, meta, torch.full_like(meta, np.nan)))
+        got = hqq.hqq_kv_attention(cache, q, tc, lc, window=w, return_lse=True)
+        assert torch.equal(bits(got[0]), bits(want[0])) and torch.equal(got[1], want[1])
+    cache = random_cache(hqq, rng, pages, kv, D, ps, nb, g)
+    bad = t.copy()
+    bad[0, 2], bad[0, 100], bad[2, 0], bad[2, 9], bad[1, :] = -5, pages, -2 ** 31, 2 ** 31 - 1, -1
+    hidden = [np.zeros(n, bool) for n in lens]
+    for b, p in ((0, 2), (0, 100), (2, 0), (2, 9)):
+        hidden[b][p * ps:(p + 1) * ps] = True
+    hidden[1][:] = True
+    out, lse = hqq.hqq_kv_attention(cache, q, torch.from_numpy(bad).cuda(), lc, return_lse=True)
+    check(out, lse, attend(cache, q.float().cpu().numpy(), t, lens, hidden=hidden))
+    cut = torch.tensor([2 ** 31 - 1, -3, 1250], dtype=torch.int32).cuda()
+    out, lse = hqq.hqq_kv_attention(cache, q, tc, cut, max_len=1205, return_lse=True)
+    check(out, lse, attend(cache, q.float().cpu().numpy(), t, [1205, 0, 1205]))
+
+
+@pytest.mark.parametrize("D,nb,g,window", [(128, 4, 64, 0), (64, 2, 32, 700), (256, 8, 128, 0)])
+def test_a_piece_of_a_prompt(hqq, D, nb, g, window):  # noqa: F811
+    # a hundred queries a sequence over a cached context, more queries than tokens among them
+    rng = np.random.default_rng(D)
+    lens, ps, kv, heads, nq = [1500, 100, 37], 32, 2, 6, 100
+    pages = sum(-(-n // ps) for n in lens)
+    cache = random_cache(hqq, rng, pages, kv, D, ps, nb, g)
+    t = tables_of(rng, pages, lens, ps, -(-1500 // ps))
+    q = torch.from_numpy(rng.standard_normal((3, nq, heads, D)).astype(np.float32)).cuda().to(F16)
+    out, lse = hqq.hqq_kv_attention(cache, q, torch.from_numpy(t).cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                                    window=window, return_lse=True)
+    check(out, lse, attend(cache, q.float().cpu().numpy(), t, lens, window))
