@@ -327,6 +327,9 @@ def hqq_kv_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int = 
     """An empty KVCache (every row reads as zeros)."""
     if num_pages < 0 or nbits not in (2, 4, 8) or group_size not in (32, 64, 128) or head_dim % group_size:
         raise HqqError("hqq_kv_cache: nbits must be 2, 4 or 8, group_size 32, 64 or 128 and divide head_dim")
+    if kv_heads < 1 or head_dim not in (64, 128, 256) or not 16 <= page_size <= 1024 or page_size & (page_size - 1):
+        raise HqqError("hqq_kv_cache: head_dim must be 64, 128 or 256, page_size a power of two from 16 to 1024, "
+                       "kv_heads at least 1")
     codes = (num_pages, kv_heads, page_size, head_dim * nbits // 8)
     meta = (num_pages, kv_heads, page_size, head_dim // group_size, 2)
     return KVCache(torch.zeros(codes, dtype=torch.uint8, device=device),

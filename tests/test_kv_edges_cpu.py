@@ -3,7 +3,8 @@ import ctypes
 
 import pytest
 
-from test_kv_cpu import L, cache  # noqa: F401
+from free_weight_quantization_b200 import hqq
+from test_kv_cpu import ARG, FAKE, UNSUPPORTED, L, append, attend, cache, read  # noqa: F401
 
 pytest.importorskip("torch")
 
@@ -17,3 +18,12 @@ def test_a_window_that_hides_nothing_is_planned_as_none(L, batch, nq, max_len): 
     assert none > 0 or max_len <= 1024
     for window in (max_len, max_len + 1, 2 ** 31 - 1, 2 ** 31, 2 ** 63 - 17 - nq, 2 ** 63 - 17, 2 ** 63 - 16, 2 ** 63 - 2, 2 ** 63 - 1):
         assert ws(window) == none, window
+
+
+@pytest.mark.parametrize("what", [dict(kv_heads=-1), dict(kv_heads=0), dict(page_size=-16), dict(page_size=0), dict(page_size=48),
+                                  dict(page_size=1 << 40), dict(head_dim=-64), dict(head_dim=0), dict(head_dim=1 << 40),
+                                  dict(num_pages=-1)])
+def test_a_cache_of_impossible_sizes_is_refused_before_it_is_allocated(what):
+    sizes = dict(dict(num_pages=2, kv_heads=1, head_dim=128, page_size=16), **what)
+    with pytest.raises(hqq.HqqError, match="hqq_kv_cache"):
+        hqq.hqq_kv_cache(**sizes, device="cpu")
