@@ -1,8 +1,9 @@
 """Builds the CUDA library libhqq_b200.so in-tree with nvcc for sm_100a.
 
-The library is eight translation units (the C ABI, the stream engine, the tile engine in two
+The library is nine translation units (the C ABI, the stream engine, the tile engine in two
 parts, dequantize + the one-vector forward product, the tensor-core product of a batch, and the
-key/value cache's store and attention), compiled in parallel and linked into one shared object.
+key/value cache's store, attention and shared prefix), compiled in parallel and linked into one
+shared object.
 """
 from __future__ import annotations
 

@@ -275,6 +275,8 @@ def err_trace_ints(t: torch.Tensor, n: int) -> list[int]:
 
 
 # ---- the key/value cache (hqq_kv_* in the header) ------------------------------------------
+# These calls are for serving and have no backward pass: what they return requires no grad, whatever
+# their inputs require.
 
 _KV_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 
@@ -391,7 +393,8 @@ def hqq_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch
     """Quantizes keys and values [tokens, kv_heads, head_dim] (fp16 or bf16; tokens and heads may be
     strided, as slices of a fused projection are) into `slots` (int64 page * page_size + offset;
     negative: skipped) of the cache.  With return_values (or out=(k, v)) also returns the values that
-    the cache now stands for.  See hqq_kv_append in the header."""
+    the cache now stands for.  Rounding has no gradient: k and v are taken without theirs.  See
+    hqq_kv_append in the header."""
     tokens = _kv_slots(cache, slots)
     _kv_rows("k", cache, k, tokens)
     _kv_rows("v", cache, v, tokens)
@@ -504,7 +507,8 @@ def hqq_kv_attention(cache: KVCache, q: torch.Tensor, pages: torch.Tensor, lens:
     strided in all but the last dimension), over its cached context: pages int32 [batch, max_pages],
     lens int32 [batch] with the queries' own tokens counted.  Returns out (and, with return_lse, the
     binary32 log-sum-exp [batch, nq, heads]).  scale defaults to head_dim ** -0.5; max_len bounds lens
-    (default: what `pages` has room for) and sizes the launch.  See hqq_kv_attention in the header."""
+    (default: what `pages` has room for) and sizes the launch.  For serving: out and lse require no
+    grad, even if q does.  See hqq_kv_attention in the header."""
     return _kv_attend(cache, q, pages, lens, None, window, scale, max_len, out, return_lse,
                       workspace, stream)
 
@@ -517,6 +521,6 @@ def hqq_kv_prefix_attention(cache: KVCache, q: torch.Tensor, prefix_pages: torch
                             stream: torch.cuda.Stream | None = None):
     """hqq_kv_attention for a batch whose sequences share their first prefix_len tokens, held in
     prefix_pages (int32 [n]) and read once for all; pages and lens are each sequence's own tokens
-    behind it.  See hqq_kv_prefix_attention in the header."""
+    behind it.  As there, no gradients.  See hqq_kv_prefix_attention in the header."""
     return _kv_attend(cache, q, pages, lens, (prefix_pages, prefix_len), 0, scale, max_len,
                       out, return_lse, workspace, stream)

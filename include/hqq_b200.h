@@ -227,7 +227,8 @@ int hqq_shrink_lp(const float *r, int64_t n, double beta, double p, float *out, 
  *   codes [num_pages][kv_heads][page_size][head_dim * nbits / 8] bytes, for keys and for values
  *   meta  [num_pages][kv_heads][page_size][head_dim / group_size][2] fp16 (scale, zero)
  *   nbits 2, 4 or 8; head_dim 64, 128 or 256; group_size 32, 64 or 128, dividing head_dim;
- *   page_size a power of two, 16 to 1024; every pointer 16-byte aligned.
+ *   page_size a power of two, 16 to 1024; every pointer 16-byte aligned; kv_heads <= 65535,
+ *   num_pages * page_size * kv_heads <= 2^34.  Metadata are finite and scales not negative.
  * Element d = c * group_size + p * (group_size / P) + i of a row (0 <= i < group_size / P) is its
  * code number p * (head_dim / P) + c * (group_size / P) + i, P = 4 for keys and 8 for values, and
  * codes are packed lowest number in the lowest bits.  A slot is page * page_size + offset.
@@ -258,6 +259,11 @@ typedef struct hqq_kv_cache {
  *             metadata afterwards
  *   k_values, v_values  [tokens][kv_heads][head_dim] of dtype, 16-byte aligned, nullable
  *             (outputs): what hqq_kv_read gives for these slots (zeros for a token not written)
+ * The stored metadata are finite whatever is written.  A group that reaches to the end of fp16's
+ * range may stand for values a little beyond it (its scale and zero point are rounded, the latter
+ * to half a step; 65567 for +-65504 in 8 bits), which fp16 has not: read as fp16 those are
+ * infinite, as every conversion to fp16 makes them; as bf16, and as keys of an attention, finite.
+ * Limit: tokens * kv_heads < 2^31.
  * Returns HQQ_OK (tokens = 0: nothing launched) or an HQQ_ERR_* code.
  */
 int hqq_kv_append(const hqq_kv_cache_t *cache, const void *k, const void *v, int dtype,
@@ -283,9 +289,11 @@ size_t hqq_kv_attention_workspace_bytes(const hqq_kv_cache_t *cache, int64_t bat
  *     out = sum_t p_t v_t / sum_t p_t,   p_t = exp(scale * q . k_t),   lse = log(sum_t p_t)
  * k_t, v_t: the rows (code - zero) * scale, unrounded.  Query i of a sequence of len tokens is at
  * position len - nq + i; it sees the tokens up to its own position, and with window > 0 only the
- * last `window` of those.  Where it sees none, out is 0 and lse is -infinity.  The sums are
- * binary32; on the value side p_t times the group's scale is rounded to fp16 (relative to the
- * largest), once for codes and zero points alike.
+ * last `window` of those (max_len or more: all).  Where it sees none, out is 0 and lse is -infinity.
+ * Scores and sums are binary32; a query element below 2^-20 of its row's largest may lose bits to
+ * fp16's subnormal numbers.  On the value side p_t times the group's scale is rounded to fp16, once
+ * for codes and zero points alike: by half a step, or, with the largest p_t at 1, by 2^-29 of the
+ * largest scale that the group has among the sequence's values, where that is more.
  *   q         [batch][nq][heads][head_dim], 2-byte aligned, with the given strides (in values);
  *             heads a multiple of kv_heads, query head h reads key head h / (heads / kv_heads).
  *             A row with a NaN, a magnitude of 2^100 or more or of 2^84 / (scale log2 e) or more, or
@@ -301,8 +309,9 @@ size_t hqq_kv_attention_workspace_bytes(const hqq_kv_cache_t *cache, int64_t bat
  *   lse       [batch][nq][heads] binary32, nullable (output)
  *   workspace >= hqq_kv_attention_workspace_bytes(..) bytes, 16-byte aligned; contents on entry do
  *             not matter; must not be used by anything else until this call's work has finished
- * Results do not depend on what else runs: sums are joined in a fixed order.
- * Limits: batch, nq <= 65535, max_len < 2^31, heads * batch * nq < 2^31.
+ * The same call gives the same bits again, whatever else runs: sums are joined in a fixed order.
+ * Limits: batch, nq <= 65535, max_len < 2^31, heads * batch * nq < 2^31, and batch * kv_heads *
+ * ceil(nq * heads / kv_heads / 8) * (max_len / 64 + 4) < 2^31.
  */
 int hqq_kv_attention(const hqq_kv_cache_t *cache, const void *q, int dtype, int64_t batch, int64_t nq,
                      int64_t heads, int64_t q_batch_stride, int64_t q_token_stride,
@@ -318,7 +327,12 @@ int hqq_kv_attention(const hqq_kv_cache_t *cache, const void *q, int dtype, int6
  * page may be partly filled (a sequence's own tokens begin on a page of their own).  The queries
  * are the last nq tokens of prefix and own tokens together.  With more than 64 query rows (batch *
  * nq * heads / kv_heads) on a key head and group_size >= 64, head_dim <= 128 the prefix runs on the
- * tcgen05 tensor cores; p_t and the values (code - zero) * scale are then rounded to fp16, once each.
+ * tcgen05 tensor cores.  There p_t is rounded to fp16, and so are the values (code - zero) * scale
+ * (by half a step, or 2^-24 of the group's largest scale so far), after 128 (8-bit codes: 32768) has
+ * been added to the zero point in binary32 and taken off again, 2^-17 (2^-9) of a step; a key's zero
+ * point below 2^-8 is off by up to 2^-19 of a step, and the sums of q that it is multiplied by enter
+ * in two fp16 parts, 2^-22 of them.
+ * Limits: as above, prefix_len < 2^31, and batch * nq * heads / kv_heads <= 524280.
  */
 int hqq_kv_prefix_attention(const hqq_kv_cache_t *cache, const void *q, int dtype, int64_t batch,
                             int64_t nq, int64_t heads, int64_t q_batch_stride,

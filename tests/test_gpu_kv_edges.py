@@ -290,3 +290,41 @@ def test_a_piece_of_a_prompt(hqq, D, nb, g, window):  # noqa: F811
     out, lse = hqq.hqq_kv_attention(cache, q, torch.from_numpy(t).cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
                                     window=window, return_lse=True)
     check(out, lse, attend(cache, q.float().cpu().numpy(), t, lens, window))
+
+
+@pytest.mark.parametrize("nb", [2, 4, 8])
+def test_rows_at_the_end_of_the_range(hqq, nb):  # noqa: F811
+    # infinities, NaN and the largest numbers: finite metadata, finite as bf16 and in attention; as fp16
+    # what lies beyond 65504 is infinite, as the conversion makes it
+    D, ps, n = 128, 16, 6
+    for dtype in (F16, BF16):
+        cache = hqq.hqq_kv_cache(1, 1, D, ps, nb, 64)
+        k = torch.randn(n, 1, D, device="cuda").to(dtype)
+        k[0, 0, :2] = torch.tensor([np.inf, -np.inf])
+        k[1, 0, 3], k[2], k[3, 0, 70] = np.nan, np.inf, -65504.0
+        k[4, 0, ::2], k[4, 0, 1::2] = 65504.0, -65504.0
+        v = k.flip(0).contiguous()
+        slots = torch.arange(n, device="cuda")
+        hqq.hqq_kv_append(cache, k, v, slots)
+        assert torch.isfinite(cache.k_meta).all() and torch.isfinite(cache.v_meta).all()
+        as_bf, as_half = hqq.hqq_kv_read(cache, slots, BF16), hqq.hqq_kv_read(cache, slots, F16)
+        table = np.zeros((1, 1), np.int32)
+        values = [torch.from_numpy(x).cuda().transpose(0, 1) for x in context(cache, table[0], n)[::2][:2]]
+        for bf, half, x in zip(as_bf, as_half, values):
+            assert torch.isfinite(bf).all() and x.abs().max() < 65504 * (1 + 2.0 ** -8)
+            assert torch.equal(torch.isinf(half), x.abs() >= 65520)
+        q = torch.randn(1, 1, 2, D, device="cuda").to(BF16)
+        out, lse = hqq.hqq_kv_attention(cache, q, torch.from_numpy(table).cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"),
+                                        return_lse=True)
+        check(out, lse, attend(cache, q.float().cpu().numpy(), table, [n]))
+
+
+def test_results_require_no_grad(hqq):  # noqa: F811
+    cache = hqq.hqq_kv_cache(2, 1, 64, 16, 4, 32)
+    k = torch.randn(4, 1, 64, device="cuda").to(BF16).requires_grad_()
+    slots = torch.arange(4, device="cuda")
+    assert not any(x.requires_grad for x in hqq.hqq_kv_append(cache, k, k, slots, return_values=True))
+    q = torch.randn(1, 1, 2, 64, device="cuda").to(BF16).requires_grad_()
+    t, n = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.tensor([4], dtype=torch.int32, device="cuda")
+    assert not any(x.requires_grad for x in hqq.hqq_kv_attention(cache, q, t, n, return_lse=True))
+    assert not any(x.requires_grad for x in hqq.hqq_kv_prefix_attention(cache, q, t[0], 4, t, n - 4, return_lse=True))

@@ -27,3 +27,21 @@ def test_a_cache_of_impossible_sizes_is_refused_before_it_is_allocated(what):
     sizes = dict(dict(num_pages=2, kv_heads=1, head_dim=128, page_size=16), **what)
     with pytest.raises(hqq.HqqError, match="hqq_kv_cache"):
         hqq.hqq_kv_cache(**sizes, device="cpu")
+
+
+def test_scales_out_of_range_are_refused(L):  # noqa: F811
+    c = cache()
+    for scale in (3e38, 2.4e38, 1e39, -1.0, 0.0, 1e-50):
+        assert attend(L, c, scale=scale) == ARG
+        assert attend(L, c, prefix=(FAKE, 64), scale=scale) == ARG
+
+
+def test_limits_of_the_attention_calls(L):  # noqa: F811
+    c = cache(heads=1, dim=128)
+    assert attend(L, c, batch=65535, heads=8, wide=1 << 26, max_len=1 << 30) == UNSUPPORTED     # pairs * units
+    assert attend(L, c, batch=65535, nq=65535, heads=1) == UNSUPPORTED                           # rows
+    c = cache(heads=1, dim=256, group=128)
+    assert attend(L, c, prefix=(FAKE, 64), batch=65535, nq=9, heads=1) == UNSUPPORTED            # blocks of the prefix's rows
+    assert append(L, cache(heads=65535), tokens=32769) == UNSUPPORTED
+    assert append(L, cache(heads=65536)) == UNSUPPORTED
+    assert read(L, cache(pages=(1 << 27) + 1, heads=2)) == UNSUPPORTED                           # 2^34 rows
