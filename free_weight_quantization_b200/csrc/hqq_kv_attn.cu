@@ -9,7 +9,7 @@
 //   sum_t p_rt v_td = sum_t w_rtg c_td - sum_t w_rtg vz_tg,               w_rtg = p_rt vs_tg
 // so no value is rounded to 16 bits on the key side (a code is a whole number below 256, and q a
 // 16-bit number; each product is exact in binary32), and on the value side only w is, to fp16,
-// once for both sums.
+// once for both sums, relative to a power of two of its group.
 //
 // A code needs no conversion either: a field of up to 8 low bits in a 16-bit half is the fp16
 // subnormal code * 2^-24, and one that sits s bits higher code * 2^(s - 24), which the tensor
@@ -33,13 +33,13 @@
 // the device.  A pair of a sequence and a key head that is cut between CTAs leaves its parts in
 // the workspace, and hqq_kv_join_kernel joins them in the order of the tokens.
 //
-// What bounds it: per block of 16 tokens a warp has some 310 instructions at 4 bits and D = 128, 104
-// of them to take the codes apart, and the integer units issue every other cycle.  Between 8192 and
-// 16384 tokens of 64 sequences x 8 key heads a token more costs 1.19 of what its bytes cost at the
-// card's copy rate (6.55 TB/s); a call of 64 x 4096 takes 77 us (46 for its bytes), of which some 20
-// are the way in (lengths, page table, first codes: three trips to memory), the change from one pair
-// to the next, and the join.  2-bit codes take the same instructions for half the bytes (74 us, 26
-// for the bytes); 16 rows a CTA 119 us for twice the products.
+// What bounds it: per block of 16 tokens a warp has 296 instructions at 4 bits and D = 128 (290 at 2
+// bits), and the integer units issue every other cycle.  Between 8192 and 16384 tokens of 64
+// sequences x 8 key heads a token more costs 1.19 of what its bytes cost at the card's copy rate
+// (6.55 TB/s); a call of 64 x 4096 takes 76 us (46 for its bytes), of which some 20 are the way in
+// (lengths, page table, first codes: three trips to memory), the change from one pair to the next,
+// and the join.  2-bit codes take the same instructions for half the bytes (74 us, 26 for the bytes);
+// 16 rows a CTA 118 us for twice the products; 32 rows, a second pass over the codes, 207.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -881,8 +881,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) hqq_kv_join_kernel(const Attn
 }
 
 // Rows of a key head over the whole batch above which the prefix goes to the tcgen05 kernel, which
-// takes 128 at a time.  In us, 8 key heads, that kernel / the one above: 4096 tokens 32 rows 25 / 21,
-// 64 rows 25 / 22, 128 rows 27 / 30; 32768 tokens 32 rows 57 / 39, 64 rows 58 / 59.
+// takes 128 at a time.  Whole calls in us, that kernel / the one above, 4 bits, D = 128, g = 64:
+//   8 key heads   4096 tokens 32 rows 22 / 18, 64 rows 23 / 20, 128 rows 25 / 31;
+//                 32768 tokens 32 rows 56 / 38, 64 rows 57 / 60, 128 rows 60 / 115
+//   2 key heads   128 rows, 4096 tokens 23 / 19, 32768 tokens 37 / 39
+//   1 key head    128 rows, 1000 tokens 21 / 12, 4096 tokens 22 / 13, 32768 tokens 28 / 29
+// 2 and 8 bits and D = 64 lie alike (8 key heads, 128 rows x 32768: 58 / 110, 68 / 113, 41 / 74).  So
+// the rule is right where the prefix's work fills the GPU, and costs up to 9 us where one or two key
+// heads have a short one.
 constexpr int kTcMinRows = 64;
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -915,10 +921,15 @@ int make_attn_plan(const hqq_kv_cache_t *cache, int64_t batch, int64_t nq, int64
     int64_t span = max_len;
     if (window > 0) span = std::min<int64_t>(span, window + nq + kBlock);
     const int64_t units = kFixed + std::max<int64_t>(1, ceil_div(span, kUnit)), pairs = batch * c.heads * pl->row_blocks;
-    // Pairs of at most 1024 tokens have a CTA each, and no join: one launch, and no more steps in a
-    // row than the join costs.  Longer ones are shared among all SMs; a share is at least 4 units.
-    // In us, a CTA each / shared (32 heads on 8): 1 x 1000 tokens 12 / 12, 16 x 1000 14 / 18,
-    // 64 x 1000 26 / 34; 1 x 2000 20 / 12, 16 x 2000 20 / 21.
+    // Pairs of at most 1024 tokens have a CTA each, and no join: one launch, and about as many steps in
+    // a row as the join costs.  Longer ones are shared among all SMs; a share is at least 4 units.
+    // In us, a CTA each / shared, 4 bits, g = 64:
+    //   32 heads on 8, D = 128   1 x 500 tokens 8.1 / 9.9, 1 x 1000 11.7 / 10.0, 16 x 1000 12.3 / 16.1,
+    //                            64 x 1000 23.8 / 31.7, 1 x 2000 18.2 / 10.3, 16 x 2000 19.7 / 20.4
+    //   the same, D = 64         1 x 1000 9.2 / 9.1, 16 x 1000 9.6 / 13.0; D = 256: 15.8 / 11.9, 17.0 / 21.5
+    //   8 heads on 1, D = 128    1 x 500 8.3 / 9.9, 1 x 1000 11.9 / 10.0, 16 x 1000 12.3 / 10.7, 64 x 1000 12.5 / 14.0
+    // So a call of few pairs near 1024 tokens loses up to 2 us (D = 256: 4) to the rule, one of many
+    // gains up to 8.
     if (units > kFixed + 16)
         pl->ctas = (int)std::min<int64_t>(kSms * per_sm, std::max<int64_t>(pairs, ceil_div(pairs * units, 4)));
     if (pairs > INT32_MAX / units) return HQQ_ERR_UNSUPPORTED;  // units are counted in 31 bits

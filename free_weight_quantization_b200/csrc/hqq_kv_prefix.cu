@@ -28,11 +28,11 @@
 //
 // What bounds it: the turn of a tile, scores - weights - products, which tensor memory leaves no room
 // to overlap within a CTA (S of two groups and O fill its 256 columns).  64 sequences x 32 heads
-// behind 32768 tokens, 8 key heads, 4 bits, g = 64: 85 us, half of the issue slots, 400 TFLOP/s; the
+// behind 32768 tokens, 8 key heads, 4 bits, g = 64: 91 us, half of the issue slots, 380 TFLOP/s; the
 // products alone would take 21.
 //
-// Waits on mbarriers are bounded: one that runs out (none should) makes the CTA write NaN; the other
-// roles' waits run out in their turn, and the CTA ends.
+// Waits on mbarriers are bounded: one that runs out (none should) makes the CTA write NaN, which the
+// join passes on; the other roles' waits run out in their turn, and the CTA ends once its products have.
 #include <type_traits>
 
 #include "hqq_kv_attn.cuh"
