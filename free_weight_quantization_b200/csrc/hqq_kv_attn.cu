@@ -1011,7 +1011,7 @@ int check_attention(const hqq_kv_cache_t *cache, const void *q, int dtype, int64
                     const int32_t *pages, int64_t max_pages, const int32_t *lens, int64_t max_len, float scale,
                     void *out, float *lse, void *workspace, size_t workspace_bytes, const AttnPlan &pl) {
     if (dtype != HQQ_FP16 && dtype != HQQ_BF16) return HQQ_ERR_ARG;
-    if (max_pages < 0 || max_len > max_pages * (int64_t)cache->page_size || !(scale > 0.0f) || !std::isfinite(scale * kLog2e))
+    if (max_pages < 0 || ceil_div(max_len, cache->page_size) > max_pages || !(scale > 0.0f) || !std::isfinite(scale * kLog2e))
         return HQQ_ERR_ARG;
     if (batch == 0 || nq == 0) return HQQ_OK;
     if (!q || !lens || !out || (max_pages > 0 && !pages)) return HQQ_ERR_ARG;

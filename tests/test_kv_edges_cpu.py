@@ -4,7 +4,7 @@ import ctypes
 import pytest
 
 from free_weight_quantization_b200 import hqq
-from test_kv_cpu import ARG, FAKE, UNSUPPORTED, L, append, attend, cache, read  # noqa: F401
+from test_kv_cpu import ARG, FAKE, UNSUPPORTED, WORKSPACE, L, append, attend, cache, read  # noqa: F401
 
 pytest.importorskip("torch")
 
@@ -45,3 +45,13 @@ def test_limits_of_the_attention_calls(L):  # noqa: F811
     assert append(L, cache(heads=65535), tokens=32769) == UNSUPPORTED
     assert append(L, cache(heads=65536)) == UNSUPPORTED
     assert read(L, cache(pages=(1 << 27) + 1, heads=2)) == UNSUPPORTED                           # 2^34 rows
+
+
+@pytest.mark.parametrize("wide", [1 << 57, 1 << 58, 1 << 60, 2 ** 63 - 1])
+def test_tables_wider_than_64_bits_of_tokens(L, wide):  # noqa: F811
+    # the table's room in tokens is not counted, so that it cannot overflow: such a call comes as far as
+    # its missing workspace
+    for prefix in (None, (FAKE, 64)):
+        assert attend(L, cache(), wide=wide, max_len=8192, ws=None, wsb=0, prefix=prefix) == WORKSPACE
+        assert attend(L, cache(), wide=127, max_len=8192, ws=None, wsb=0, prefix=prefix) == ARG
+        assert attend(L, cache(), wide=127, max_len=127 * 64, ws=None, wsb=0, prefix=prefix) == WORKSPACE
