@@ -57,8 +57,9 @@ __device__ __forceinline__ bool row_in_range(uint32_t big, float scale_log2) {
     return big < (227u << 23) && __uint_as_float(big) * scale_log2 < 0x1p84f;
 }
 
-// The largest score, in powers of two, of a row that can be answered: exp2(s unit - m) takes the
-// rounding of m = max(s) unit to the exponent, 2^-24 of the score.  Beyond, the row is made NaN.
+// The largest score of a block, in powers of two, that can be answered: the roundings of m = max(s)
+// unit and of the bound (m + kLag) / unit, 2^-24 of the score each, go to the exponent s unit - m, 0.6
+// in all at 2^22, where w is still below 2^15.7.  Beyond, the row is made NaN.
 constexpr float kScoreLimit = 0x1p22f;
 __device__ __forceinline__ bool score_in_range(float top) { return fabsf(top) < kScoreLimit || top == kLowest; }
 

@@ -228,7 +228,8 @@ int hqq_shrink_lp(const float *r, int64_t n, double beta, double p, float *out, 
  *   meta  [num_pages][kv_heads][page_size][head_dim / group_size][2] fp16 (scale, zero)
  *   nbits 2, 4 or 8; head_dim 64, 128 or 256; group_size 32, 64 or 128, dividing head_dim;
  *   page_size a power of two, 16 to 1024; every pointer 16-byte aligned; kv_heads <= 65535,
- *   num_pages * page_size * kv_heads <= 2^34.  Metadata are finite and scales not negative.
+ *   num_pages * page_size * kv_heads <= 2^34.  Metadata of rows that are read are finite, scales not
+ *   negative, zero points within +-32768 (hqq_kv_append writes some 2000 at most).
  * Element d = c * group_size + p * (group_size / P) + i of a row (0 <= i < group_size / P) is its
  * code number p * (head_dim / P) + c * (group_size / P) + i, P = 4 for keys and 8 for values, and
  * codes are packed lowest number in the lowest bits.  A slot is page * page_size + offset.
@@ -296,9 +297,10 @@ size_t hqq_kv_attention_workspace_bytes(const hqq_kv_cache_t *cache, int64_t bat
  * largest scale that the group has among the sequence's values, where that is more.
  *   q         [batch][nq][heads][head_dim], 2-byte aligned, with the given strides (in values);
  *             heads a multiple of kv_heads, query head h reads key head h / (heads / kv_heads).
- *             A row with a NaN, a magnitude of 2^100 or more or of 2^84 / (scale log2 e) or more, or
- *             a largest score (scale log2 e q . k_t) of magnitude 2^22 or more comes back as NaN, out
- *             and lse, if it sees a token
+ *             A row with a NaN or a magnitude of 2^100 or more, or of 2^84 / (scale log2 e) or more,
+ *             comes back as NaN, out and lse, if it sees a token; one with a score scale log2 e q . k_t
+ *             of magnitude 2^22 or more comes back right or as NaN, as one whose largest score is that
+ *             always does
  *   pages     [batch][max_pages] device int32, rows pages_stride apart: each sequence's pages in
  *             order.  Tokens of a page number outside the pool are not seen
  *   lens      [batch] device int32: tokens of each sequence, the queries' own among them (append

@@ -328,3 +328,40 @@ def test_results_require_no_grad(hqq):  # noqa: F811
     t, n = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.tensor([4], dtype=torch.int32, device="cuda")
     assert not any(x.requires_grad for x in hqq.hqq_kv_attention(cache, q, t, n, return_lse=True))
     assert not any(x.requires_grad for x in hqq.hqq_kv_prefix_attention(cache, q, t[0], 4, t, n - 4, return_lse=True))
+
+
+@pytest.mark.parametrize("path", ["own", "shared", "prefix", "many rows"])
+def test_scores_far_apart_are_right_or_nan(hqq, path):  # noqa: F811
+    # some tokens' scores lie at -2^19 to -2^30 and beyond, the others near zero: rows with scores below 2^22
+    # are right, the others right or NaN; nothing is silently wrong
+    rng = np.random.default_rng(8)
+    D, ps, kv, heads = 128, 16, 2, 4
+    lens = {"shared": [1500, 64, 700], "own": [500, 64, 300]}.get(path, [30, 1, 70])
+    B, nq = len(lens), 14 if path == "many rows" else 3
+    prefix = 600 if path not in ("own", "shared") else 0
+    shared = -(-prefix // ps)
+    pages = shared + sum(-(-n // ps) for n in lens)
+    t = tables_of(rng, pages - shared, lens, ps, -(-max(lens) // ps)) + shared
+    tc, lc = torch.from_numpy(t.astype(np.int32)).cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    pt = rng.permutation(shared).astype(np.int32)
+    q = torch.from_numpy(-np.abs(rng.standard_normal((B, nq, heads, D))).astype(np.float32)).cuda().to(BF16)
+    for low, high, size in ((9, 11, (pages, kv, ps, 1)), (13, 15, (pages, kv, ps, 1)), (13, 15, (pages, 1, 1, 1))):
+        cache = random_cache(hqq, rng, pages, kv, D, ps, 4, 64)
+        cache.k_meta[..., 1] = 0
+        up = 2.0 ** torch.from_numpy(rng.uniform(low, high, (pages, kv, ps, 1))).cuda()
+        up[torch.from_numpy(rng.random(size) < 0.6).cuda().expand(up.shape)] = 1   # some tokens, or whole blocks
+        cache.k_meta[..., 0] = (cache.k_meta[..., 0].double() * up).clamp(max=2.0 ** 15).half()
+        for scale in (1.0, 16.0, 1024.0):
+            if shared:
+                out, lse = hqq.hqq_kv_prefix_attention(cache, q, torch.from_numpy(pt).cuda(), prefix, tc, lc, scale=scale, return_lse=True)
+            else:
+                out, lse = hqq.hqq_kv_attention(cache, q, tc, lc, scale=scale, return_lse=True)
+            want = attend(cache, q.float().cpu().numpy(), t, lens, prefix=(pt, prefix) if shared else (None, 0), scale=scale)
+            bad = torch.isnan(lse)
+            k = np.concatenate([context(cache, x, len(x) * ps)[0] for y in (pt[None], t) for x in y if len(x)], 1)
+            rows = np.abs(q.float().cpu().numpy().astype(np.float64)).sum(-1).max()
+            if scale * np.log2(np.e) * rows * np.abs(k).max() < 2.0 ** 22:
+                assert not bad.any()
+            assert torch.isnan(out[bad]).all()
+            out[bad], lse[bad] = torch.from_numpy(want[0]).cuda().to(out)[bad], torch.from_numpy(want[1]).cuda().to(lse)[bad]
+            check(out, lse, want, (low, scale))
